@@ -23,8 +23,8 @@
  *  - Pointers named "device" are CUDA device pointers on the current device;
  *    pointers named "host" are ordinary host memory.  `stream` is a
  *    cudaStream_t (NULL = legacy default stream).  All device work is enqueued
- *    asynchronously on `stream`; only rswa_state_create, rswa_get_ring and
- *    rswa_check_device_error synchronise.
+ *    asynchronously on `stream`; only rswa_state_create, rswa_tree_create,
+ *    rswa_get_ring and rswa_check_device_error synchronise.
  *  - OWNERSHIP: the caller owns ALL device memory (inputs, outputs, K/V
  *    caches, workspace).  The library never allocates or frees device memory;
  *    it keeps raw pointers inside the opaque host-side state.
@@ -372,6 +372,137 @@ rswa_status rswa_ngram_topk(float *logits, int64_t ld, const int32_t *history, i
                             const float *uniform, float temperature, int32_t *top_idx,
                             float *top_val, int32_t *token, int32_t *device_error, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens (speculative decoding).  A step drafts up to T
+ * tokens a sequence; node i continues node parent[i] < i, or the committed
+ * tokens where parent[i] = -1.  With t_b tokens generated so far, node i at
+ * depth e (0 for a first node) stands for generated token t_b + e, and
+ * rswa_tree_attention gives it the output that e + 1 calls of
+ * rswa_decode_step down its path would give it:
+ *   - every prompt entry of its sequence;
+ *   - the ring entries whose token number is at least t_b + e - W + 1 (the
+ *     ones that deeper steps would already have overwritten are left out);
+ *   - the nodes above it and itself, as far up as the window of W reaches;
+ * and no other node.  In the standard sliding-window mode the window cuts the
+ * prompt too.  The cache is only read.  rswa_tree_commit then writes the path
+ * that the caller's model confirmed into the rings of all layers, and
+ * rswa_tree_advance adds its length to the ring counters.  With RoPE on, q and
+ * k_draft are turned at their nodes' positions, and the cache receives turned
+ * keys; a turned q or key counts as rounded to the element type.
+ *
+ * One step:  rswa_tree_set, rswa_tree_attention once a layer, rswa_tree_commit,
+ * rswa_tree_advance.  All four may be captured in a CUDA graph.  Calls on one
+ * tree share its workspace: order them on one stream (two graphs that use the
+ * same tree must not run at the same time).
+ * ------------------------------------------------------------------------ */
+typedef struct rswa_tree rswa_tree;
+#define RSWA_TREE_MAX 128
+
+/* Bytes of device workspace rswa_tree_create needs for trees of up to
+ * max_draft nodes (1 <= max_draft <= RSWA_TREE_MAX) over this state: the work
+ * plan, masks, and the partial results of split rings.  Call it with the
+ * state's device current.  0 if invalid. */
+size_t rswa_tree_workspace_bytes(const rswa_state *state, int32_t max_draft);
+
+/* A tree over `state`, which must outlive it.  T = max_draft is the row stride
+ * of every [B][T] array below.  workspace: device, 256-byte aligned, owned by
+ * the caller, used by the tree until rswa_tree_destroy.  Uploads its tables on
+ * `stream` and synchronises it.  RSWA_EINVAL, RSWA_ENOMEM (workspace too
+ * small) or RSWA_ECUDA. */
+rswa_status rswa_tree_create(rswa_state *state, int32_t max_draft, void *workspace,
+                             size_t workspace_size, void *stream, rswa_tree **out);
+
+/* Free the host-side object.  Device memory stays the caller's. */
+rswa_status rswa_tree_destroy(rswa_tree *tree);
+
+/* The step's drafts.
+ *  parent  : device int32 [B][T], -1 <= parent[b][i] < i for i < n_draft[b]
+ *            (the rest is not looked at); NULL: chains (parent[i] = i - 1).
+ *  n_draft : device int32 [B], 0 <= n_draft[b] <= T, or NULL (all T).
+ * A sequence with a bad parent or count is refused: its attention rows are left
+ * as they were, its commit takes nothing, and RSWA_DEVERR_BAD_TREE or
+ * RSWA_DEVERR_BAD_LENGTH goes into the state's device error word.  With RoPE
+ * on the nodes' positions are worked out from the ring counters here: call it
+ * after the previous step's rswa_tree_advance. */
+rswa_status rswa_tree_set(rswa_tree *tree, const int32_t *parent, const int32_t *n_draft,
+                          void *stream);
+
+/* Attention of one layer's drafted tokens.
+ *  q, k_draft, v_draft, out : device [B][T][H][d], 16-byte aligned; rows
+ *            i >= n_draft[b] are neither read nor written.
+ * Values of entries that a node does not attend to never reach its output,
+ * infinities and NaN included.  RSWA_EINVAL for a bad layer or pointer,
+ * RSWA_ESTATE as rswa_decode_step. */
+rswa_status rswa_tree_attention(rswa_tree *tree, int32_t layer, const void *q, const void *k_draft,
+                                const void *v_draft, void *out, void *stream);
+
+/* Write the accepted tokens' K/V into the rings of every layer.
+ *  k_draft, v_draft : host arrays of num_layers device pointers, as passed to
+ *            rswa_tree_attention.
+ *  path      : device int32 [B][T]: path[b][0 .. path_len[b]) are nodes, each
+ *            the parent of the next, from a first node down.
+ *  path_len  : device int32 [B], 0 <= path_len[b] <= n_draft[b].
+ * Token i of the path goes to slot P_b + ((t_b + i) mod W); of more than W
+ * tokens the last W are stored.  A sequence whose path is not such a chain is
+ * left as it was and counts 0 accepted tokens (RSWA_DEVERR_BAD_TREE /
+ * RSWA_DEVERR_BAD_LENGTH).  The counters t_b do not move. */
+rswa_status rswa_tree_commit(rswa_tree *tree, const void *const *k_draft,
+                             const void *const *v_draft, const int32_t *path,
+                             const int32_t *path_len, void *stream);
+
+/* t_b += the tokens that the last rswa_tree_commit took of sequence b (0 if it
+ * has been counted already, or after rswa_tree_set). */
+rswa_status rswa_tree_advance(rswa_tree *tree, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction of prompt entries by accumulated attention weight.  The cache of a
+ * long prompt stays at P_b + W entries for the whole output; where that is too
+ * much, decode some tokens with rswa_decode_step_scored, which adds up how much
+ * attention every entry gets, and move the most attended P'_b prompt entries of
+ * each head into a smaller cache with rswa_evict.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of one layer's score buffer: a float per cache row, the score of
+ * (b, h, slot) at index rswa_cache_offset(b, h, slot) / head_dim. */
+size_t rswa_score_bytes(const rswa_state *state);
+
+/* rswa_decode_step, and for every entry attended to
+ *   score_out[entry] = score_in[entry] + its softmax weight;
+ * the step's own ring slot starts over at its weight.  Held entries outside the
+ * window of the standard sliding-window mode keep score_in.  Floats of slots
+ * that hold no entry are not touched.
+ *  score_in, score_out : device, rswa_score_bytes() each, 16-byte aligned; may
+ *            be the same buffer (they must not overlap otherwise).
+ *  scratch : device, rswa_score_bytes(), 16-byte aligned; overwritten.  Calls
+ *            that may run at the same time need one each.
+ * Errors as rswa_decode_step. */
+rswa_status rswa_decode_step_scored(rswa_state *state, int32_t layer, const void *q,
+                                    const void *k_new, const void *v_new, void *out,
+                                    const float *score_in, float *score_out, float *scratch,
+                                    void *stream);
+
+/* Move one layer of `src` into `dst`, a state over other memory with the same
+ * config and prefill_len P'_b <= P_b: per (b, h), the P'_b prompt entries with
+ * the highest score, in slot order, then the ring's held slots at their places.
+ *  score   : device float, rswa_score_bytes(src).  Higher ranks first, the
+ *            lower slot first among equal scores; NaN ranks last.
+ *  n_first, n_last : the first n_first and the last n_last prompt entries are
+ *            kept whatever their score; min(n_first + n_last, P_b) <= P'_b.
+ *  dst_score : device float, rswa_score_bytes(dst), or NULL: the moved entries'
+ *            scores.
+ *  kept    : device int32 [H * sum_b P'_b]: the source slots of ring (b, h),
+ *            ascending, at H sum_{b' < b} P'_b' + h P'_b.
+ * 16-byte aligned pointers; nothing of dst may overlap src.  dst takes over the
+ * ring counters (also as the value that rswa_reset_ring restores), the RoPE
+ * setting and the positions: generated token t keeps position P_b + t of the
+ * uncut prompt, and under RSWA_ROPE_SLOT P_b + (t mod W).  Decode may start on
+ * the layer at once.  Ring slots that src does not hold are not written.
+ * RSWA_EINVAL also if either state is in the standard sliding-window mode;
+ * RSWA_ESTATE if src's layer was never filled. */
+rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, const float *score,
+                       int32_t n_first, int32_t n_last, float *dst_score, int32_t *kept,
+                       void *stream);
+
 /* Synchronises `stream`, then copies the ring counters to the host:
  *  n_generated : host [B] or NULL -- t_b;
  *  ring_pos    : host [B] or NULL -- the pages' ring_pos: 0 during warm-up,
@@ -484,6 +615,7 @@ int64_t rswa_debug_prefill_plan(const rswa_config *cfg, const int64_t *prefill_l
 #define RSWA_DEVERR_TIMEOUT 1
 #define RSWA_DEVERR_BAD_TOKEN 2
 #define RSWA_DEVERR_BAD_LENGTH 4
+#define RSWA_DEVERR_BAD_TREE 8
 
 #ifdef __cplusplus
 }

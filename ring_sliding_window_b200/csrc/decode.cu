@@ -162,14 +162,17 @@ struct DecodeArgs {
   const void *q, *k_new, *v_new;
   void *kc, *vc;
   void *out;
+  float *raw;  // scored step: every attended entry's score in log2 units, by cache row
 };
 
 
 // Element tid of ring bh's result: the normalised output, or, for a partial
 // step, the unnormalised (m, l, o) the caller combines with other shares.
-template <typename T, int D>
+// A scored step also leaves (m, l), which turn its raw scores into weights.
+template <typename T, int D, bool kScored>
 __device__ __forceinline__ void store_result(const DeviceView &v, const DecodeArgs &a, int bh,
                                              int tid, float m, float l, float acc) {
+  if (kScored && tid == 0) v.ring_ml[bh] = make_float2(m, l);
   if (v.out_ml) {
     v.out_o[(int64_t)bh * D + tid] = acc;
     if (tid == 0) v.out_ml[bh] = make_float2(m, l);
@@ -184,7 +187,8 @@ __device__ __forceinline__ void store_result(const DeviceView &v, const DecodeAr
 //   equal key range; partials go to the leader CTA's shared memory and one
 //   cluster barrier replaces the global publish/merge (small batches, where
 //   that hand-off dominates the step).
-template <typename T, int D, bool kCluster>
+// kScored: a scored step (rswa_decode_step_scored), which stores the raw scores.
+template <typename T, int D, bool kCluster, bool kScored>
 __global__ void __launch_bounds__(DecodeShape<T, D>::kThreads)
     decode_split_kernel(const DecodeArgs a) {
   using S = DecodeShape<T, D>;
@@ -431,6 +435,7 @@ __global__ void __launch_bounds__(DecodeShape<T, D>::kThreads)
           acc += __shfl_xor_sync(0xffffffffu, acc, 2);
           acc += __shfl_xor_sync(0xffffffffu, acc, 4);
           sc[ps] = r < rows ? acc : -INFINITY;
+          if (kScored && li == 0 && r < rows) a.raw[pc.row0 + k0 + r] = acc;
         }
         float m_new = m;
 #pragma unroll
@@ -527,7 +532,7 @@ __global__ void __launch_bounds__(DecodeShape<T, D>::kThreads)
           Lg = (l4[0] + l4[1]) + (l4[2] + l4[3]);
           acc = (a4[0] + a4[1]) + (a4[2] + a4[3]);
         }
-        store_result<T, D>(v, a, pc.b * v.H + pc.h, tid, Mg, Lg, acc);
+        store_result<T, D, kScored>(v, a, pc.b * v.H + pc.h, tid, Mg, Lg, acc);
       }
       continue;  // a cluster CTA has exactly one piece
     }
@@ -584,7 +589,7 @@ __global__ void __launch_bounds__(DecodeShape<T, D>::kThreads)
         }
         Mg = Mc;
       }
-      if (tid < D) store_result<T, D>(v, a, bh, tid, Mg, Lg, acc);
+      if (tid < D) store_result<T, D, kScored>(v, a, bh, tid, Mg, Lg, acc);
     }
   }
 }
@@ -596,29 +601,31 @@ __global__ void advance_kernel(int64_t *t, int B) {
   if (b < B) t[b] += 1;
 }
 
-template <typename T, int D, bool kCluster>
+template <typename T, int D, bool kCluster, bool kScored = false>
 cudaError_t set_smem_attr() {
   const int smem = (int)sizeof(DecodeSmem<T, D, kCluster>);
-  cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<T, D, kCluster>,
+  cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<T, D, kCluster, kScored>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && kCluster)
-    e = cudaFuncSetAttribute(decode_split_kernel<T, D, kCluster>,
+    e = cudaFuncSetAttribute(decode_split_kernel<T, D, kCluster, kScored>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
 }
 
-template <typename T, int D, bool kCluster>
+template <typename T, int D, bool kCluster, bool kScored>
 cudaError_t launch_decode_t(const DeviceView &v, const void *q, const void *k_new,
                             const void *v_new, void *kc, void *vc, void *out, cudaStream_t s,
-                            bool pdl) {
+                            bool pdl, float *raw) {
   using S = DecodeShape<T, D>;
-  static bool attr_set = false;  // per instantiation; also set when the state is built
-  if (!attr_set) {
-    cudaError_t e = set_smem_attr<T, D, kCluster>();
+  // per instantiation and device; the plain forms' are also set when the state is built
+  static bool attr_set[64] = {};
+  const int dev = current_device();
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    cudaError_t e = set_smem_attr<T, D, kCluster, kScored>();
     if (e != cudaSuccess) return e;
-    attr_set = true;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  DecodeArgs a{v, q, k_new, v_new, kc, vc, out};
+  DecodeArgs a{v, q, k_new, v_new, kc, vc, out, raw};
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(kCluster ? v.B * v.H * v.cluster_size : v.decode_grid);
   lc.blockDim = dim3(S::kThreads);
@@ -637,16 +644,20 @@ cudaError_t launch_decode_t(const DeviceView &v, const void *q, const void *k_ne
   }
   lc.attrs = attr;
   lc.numAttrs = na;
-  return cudaLaunchKernelEx(&lc, decode_split_kernel<T, D, kCluster>, a);
+  return cudaLaunchKernelEx(&lc, decode_split_kernel<T, D, kCluster, kScored>, a);
 }
 
 template <typename T, int D>
 cudaError_t launch_decode_d(const DeviceView &v, const void *q, const void *k_new,
                             const void *v_new, void *kc, void *vc, void *out, cudaStream_t s,
-                            bool pdl) {
+                            bool pdl, float *raw) {
+  if (raw)
+    return v.cluster_size > 0
+               ? launch_decode_t<T, D, true, true>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw)
+               : launch_decode_t<T, D, false, true>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
   return v.cluster_size > 0
-             ? launch_decode_t<T, D, true>(v, q, k_new, v_new, kc, vc, out, s, pdl)
-             : launch_decode_t<T, D, false>(v, q, k_new, v_new, kc, vc, out, s, pdl);
+             ? launch_decode_t<T, D, true, false>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw)
+             : launch_decode_t<T, D, false, false>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
 }
 
 template <typename T, int D>
@@ -654,7 +665,7 @@ int ctas_per_sm_t() {
   using S = DecodeShape<T, D>;
   if (set_smem_attr<T, D, false>() != cudaSuccess) return 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<T, D, false>,
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<T, D, false, false>,
                                                     S::kThreads,
                                                     sizeof(DecodeSmem<T, D, false>)) !=
           cudaSuccess ||
@@ -680,7 +691,7 @@ int max_clusters_t(int cluster) {
   lc.attrs = attr;
   lc.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, decode_split_kernel<T, D, true>, &lc) != cudaSuccess)
+  if (cudaOccupancyMaxActiveClusters(&n, decode_split_kernel<T, D, true, false>, &lc) != cudaSuccess)
     return 0;
   return n;
 }
@@ -689,14 +700,14 @@ int max_clusters_t(int cluster) {
 
 cudaError_t launch_decode(const DeviceView &v, const void *q, const void *k_new,
                           const void *v_new, void *kc, void *vc, void *out, cudaStream_t s,
-                          bool pdl) {
+                          bool pdl, float *raw) {
   if (v.dtype == RSWA_BF16) {
     if (v.D == 128)
-      return launch_decode_d<__nv_bfloat16, 128>(v, q, k_new, v_new, kc, vc, out, s, pdl);
-    return launch_decode_d<__nv_bfloat16, 64>(v, q, k_new, v_new, kc, vc, out, s, pdl);
+      return launch_decode_d<__nv_bfloat16, 128>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
+    return launch_decode_d<__nv_bfloat16, 64>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
   }
-  if (v.D == 128) return launch_decode_d<float, 128>(v, q, k_new, v_new, kc, vc, out, s, pdl);
-  return launch_decode_d<float, 64>(v, q, k_new, v_new, kc, vc, out, s, pdl);
+  if (v.D == 128) return launch_decode_d<float, 128>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
+  return launch_decode_d<float, 64>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
 }
 
 // Log-sum-exp merge of `shares` partials (m, l, o) per ring: one CTA per ring,

@@ -32,6 +32,7 @@ struct WsLayout {
   size_t err;        // int32 device error word (+ int32 debug flags)
   size_t t;          // int64 [B]   tokens generated so far
   size_t plen;       // int32 [B]   P_b
+  size_t pos_base;   // int32 [B]   prompt length that positions count from
   size_t slot_base;  // int64 [B+1] first cache slot of each request
   size_t tok_base;   // int64 [B+1] sum_{b'<b} P_b'
   size_t tile_base;  // int32 [B+1] sum_{b'<b} ceil(P_b' / kPrefillTile)
@@ -44,6 +45,7 @@ struct WsLayout {
   size_t part_ml;    // float2 [n_pieces] (running max in log2 units, sum)
   size_t part_o;     // float [n_pieces][d] unnormalised outputs
   size_t rope_cs;    // float2 [B][d/2] (cos, sin) at each request's current position
+  size_t ring_ml;    // float2 [B*H] softmax max (log2 units) and sum of a scored step
   size_t total;
 };
 
@@ -93,10 +95,30 @@ struct DeviceView {
   int rope;          // rswa_rope_policy (0: keys and queries used as given)
   float rope_theta;
   float2 *rope_cs;   // [B][D/2] (cos, sin) of the position of each request's next token
+  int32_t *pos_base;  // [B] P_b of the positions: plen, or the uncut prompt's after an eviction
+  float2 *ring_ml;    // [B*H] (m, l) of every ring's softmax, written by a scored step
   int64_t total_tokens;  // sum P_b
   int total_tiles;       // sum ceil(P_b / kPrefillTile)
   int total_tiles64;     // sum ceil(P_b / kSimtTile)
   int max_plen;
+};
+
+// A tree of drafted tokens per sequence, as the kernels see it.
+struct TreeView {
+  int T;                     // drafted tokens a sequence (the row stride of the inputs)
+  int tile;                  // keys a tile of the work plan holds
+  int grid;                  // attention CTAs
+  const DecodePiece *pieces; // key_begin / key_end count tiles: the drafts' first, then the cache's
+  const int32_t *cta_piece;  // [grid + 1]
+  const int32_t *bh_piece;   // [B*H + 1] first piece of each ring
+  float2 *part_ml;           // [n_pieces][T]
+  float *part_o;             // [n_pieces][T][D]
+  int32_t *parent;           // [B][T] as given to rswa_tree_set
+  int32_t *depth;            // [B][T]
+  uint4 *above;              // [B][T] bit j: row i attends to draft j (an ancestor or itself)
+  int32_t *n;                // [B] drafted tokens in use (0: the sequence's tree was refused)
+  int32_t *accepted;         // [B] tokens the last commit took, until rswa_tree_advance
+  float2 *cs;                // [B][T][D/2] (cos, sin) at every draft's position (RoPE)
 };
 
 }  // namespace rswa
@@ -122,9 +144,11 @@ namespace rswa {
 // Launchers (return cudaGetLastError() of their launch).
 // pdl: launch with programmatic stream serialization (the kernel waits for
 // the previous kernel's completion before touching any produced data).
+// raw: non-null makes it a scored step: every attended entry's score (log2
+// units) goes to raw[cache row] and every ring's (m, l) to v.ring_ml.
 cudaError_t launch_decode(const DeviceView &v, const void *q, const void *k_new,
                           const void *v_new, void *kc, void *vc, void *out, cudaStream_t s,
-                          bool pdl);
+                          bool pdl, float *raw = nullptr);
 cudaError_t launch_advance(const DeviceView &v, cudaStream_t s);
 cudaError_t launch_combine(const float2 *ml, const float *o, int shares, int64_t rings, int D,
                            int dtype, void *out, cudaStream_t s);
@@ -163,6 +187,27 @@ cudaError_t launch_ngram(float *logits, int64_t ld, const int32_t *history, int6
                          const int32_t *hist_len, int rows, int vocab, int n, int window,
                          int *err, cudaStream_t s);
 
+// Draft trees.
+cudaError_t launch_tree_set(const DeviceView &v, const TreeView &tv, const int32_t *parent,
+                            const int32_t *n_draft, cudaStream_t s);
+// (cos, sin) of every draft's position (RoPE; nothing to do without it).
+cudaError_t launch_tree_rope(const DeviceView &v, const TreeView &tv, cudaStream_t s);
+cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const void *q,
+                             const void *kd, const void *vd, const void *kc, const void *vc,
+                             void *out, cudaStream_t s);
+// CTAs of the tree attention kernel for (dtype, head_dim) that one SM holds.
+int tree_simt_ctas_per_sm(int dtype, int head_dim, int n_rows);
+// Merge of the pieces of every ring that has more than one.
+cudaError_t launch_tree_combine(const DeviceView &v, const TreeView &tv, void *out,
+                                cudaStream_t s);
+// t_b += accepted_b, accepted_b = 0, and the RoPE table of the new position.
+cudaError_t launch_tree_advance(const DeviceView &v, int32_t *accepted, cudaStream_t s);
+
+// score_out = score_in (0 at this step's ring slot) + 2^(s - m) / l over every
+// ring, with the raw scores s and (m, l) that a scored decode step left.
+cudaError_t launch_score_finish(const DeviceView &v, const float *raw, const float *score_in,
+                                float *score_out, cudaStream_t s);
+
 // Resident decode CTAs per SM for (dtype, head_dim); used by the planner.
 int decode_ctas_per_sm(int dtype, int head_dim);
 // Clusters of `cluster` decode CTAs that can be resident at once (0: none).
@@ -176,6 +221,7 @@ int sm_count(int dev);
 // packed back to back in batch order.
 DecodePlan plan_decode(const rswa_config *c, const int64_t *plen, const int64_t *slot_base,
                        int num_sms, int ctas_per_sm);
+rswa_status from_cuda(cudaError_t e);
 WsLayout layout_ws(const rswa_config *c, const int64_t *plen, const DecodePlan &p);
 
 }  // namespace rswa

@@ -107,7 +107,7 @@ __global__ void rope_table_kernel(const DeviceView v) {
   const int half = v.D / 2;
   const int b = blockIdx.x;
   const int64_t t = v.t[b];
-  const int64_t P = v.plen[b];
+  const int64_t P = v.pos_base[b];
   const int64_t pos = v.rope == RSWA_ROPE_SLOT ? P + t % v.W : P + t;
   for (int i = threadIdx.x; i < half; i += blockDim.x)
     v.rope_cs[(int64_t)b * half + i] = rope_cs(pos, i, v.D, v.rope_theta);
@@ -120,7 +120,7 @@ __global__ void advance_rope_kernel(const DeviceView v) {
   const int half = v.D / 2;
   const int b = blockIdx.x;
   const int64_t t = v.t[b] + 1;
-  const int64_t P = v.plen[b];
+  const int64_t P = v.pos_base[b];
   __syncthreads();  // every thread has read the old t
   if (threadIdx.x == 0) v.t[b] = t;
   const int64_t pos = v.rope == RSWA_ROPE_SLOT ? P + t % v.W : P + t;
@@ -128,7 +128,49 @@ __global__ void advance_rope_kernel(const DeviceView v) {
     v.rope_cs[(int64_t)b * half + i] = rope_cs(pos, i, v.D, v.rope_theta);
 }
 
+// The position of draft i of request b is that of generated token t + depth_i:
+// (cos, sin) for its query and key.  One CTA per draft.
+__global__ void __launch_bounds__(64) tree_rope_kernel(const DeviceView v, const TreeView tv) {
+  const int64_t row = blockIdx.x;
+  const int b = (int)(row / tv.T), i = (int)(row % tv.T);
+  if (i >= tv.n[b]) return;
+  const int half = v.D / 2;
+  const int64_t t = v.t[b] + tv.depth[row];
+  const int64_t P = v.pos_base[b];
+  const int64_t pos = v.rope == RSWA_ROPE_SLOT ? P + t % v.W : P + t;
+  for (int e = threadIdx.x; e < half; e += blockDim.x)
+    tv.cs[row * half + e] = rope_cs(pos, e, v.D, v.rope_theta);
+}
+
+// t_b += accepted_b, and the table for the new position with RoPE on.
+__global__ void __launch_bounds__(64) tree_advance_kernel(const DeviceView v, int32_t *accepted) {
+  const int half = v.D / 2;
+  const int b = blockIdx.x;
+  const int64_t t = v.t[b] + accepted[b];
+  __syncthreads();  // every thread has read the old counters
+  if (threadIdx.x == 0) {
+    v.t[b] = t;
+    accepted[b] = 0;
+  }
+  if (!v.rope) return;
+  const int64_t P = v.pos_base[b];
+  const int64_t pos = v.rope == RSWA_ROPE_SLOT ? P + t % v.W : P + t;
+  for (int i = threadIdx.x; i < half; i += blockDim.x)
+    v.rope_cs[(int64_t)b * half + i] = rope_cs(pos, i, v.D, v.rope_theta);
+}
+
 }  // namespace
+
+cudaError_t launch_tree_rope(const DeviceView &v, const TreeView &tv, cudaStream_t s) {
+  if (!v.rope) return cudaSuccess;
+  tree_rope_kernel<<<(unsigned)(v.B * tv.T), 64, 0, s>>>(v, tv);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_advance(const DeviceView &v, int32_t *accepted, cudaStream_t s) {
+  tree_advance_kernel<<<v.B, 64, 0, s>>>(v, accepted);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_rope_prefill(const DeviceView &v, const void *q, const void *k, void *qr,
                                 void *kc, cudaStream_t s) {

@@ -184,6 +184,7 @@ WsLayout layout_ws(const rswa_config *c, const int64_t *plen, const DecodePlan &
   w.err = off;         off = align256(off + 2 * sizeof(int32_t));
   w.t = off;           off = align256(off + 2 * B * sizeof(int64_t));  // t and its reset copy
   w.plen = off;        off = align256(off + B * sizeof(int32_t));
+  w.pos_base = off;    off = align256(off + B * sizeof(int32_t));
   w.slot_base = off;   off = align256(off + (B + 1) * sizeof(int64_t));
   w.tok_base = off;    off = align256(off + (B + 1) * sizeof(int64_t));
   w.tile_base = off;   off = align256(off + (B + 1) * sizeof(int32_t));
@@ -199,6 +200,7 @@ WsLayout layout_ws(const rswa_config *c, const int64_t *plen, const DecodePlan &
   w.part_ml = off;     off = align256(off + (size_t)p.n_pieces * sizeof(float2));
   w.part_o = off;      off = align256(off + (size_t)p.n_pieces * c->head_dim * sizeof(float));
   w.rope_cs = off;     off = align256(off + B * (size_t)(c->head_dim / 2) * sizeof(float2));
+  w.ring_ml = off;     off = align256(off + B * c->num_heads * sizeof(float2));
   w.total = off;
   return w;
 }
@@ -250,13 +252,17 @@ int choose_cluster_size(const rswa_config *c, const int64_t *plen, int num_sms) 
 
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 
+}  // namespace
+
+namespace rswa {
+
 rswa_status from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return RSWA_OK;
   g_last_cuda_error = e;
   return RSWA_ECUDA;
 }
 
-}  // namespace
+}  // namespace rswa
 
 // ---------------------------------------------------------------------------
 extern "C" {
@@ -360,6 +366,7 @@ rswa_status rswa_state_create_pooled(const rswa_config *cfg, const int64_t *pref
   auto at = [&](size_t off) { return img.data() + off; };
   int64_t *t = (int64_t *)at(s->ws.t);
   int32_t *pl = (int32_t *)at(s->ws.plen);
+  int32_t *pb = (int32_t *)at(s->ws.pos_base);
   int64_t *sb = (int64_t *)at(s->ws.slot_base);
   int64_t *tb = (int64_t *)at(s->ws.tok_base);
   int32_t *tl = (int32_t *)at(s->ws.tile_base);
@@ -368,7 +375,7 @@ rswa_status rswa_state_create_pooled(const rswa_config *cfg, const int64_t *pref
   for (int b = 0; b < B; ++b) {
     t[b] = n_generated ? n_generated[b] : 0;
     t[B + b] = t[b];  // reset copy
-    pl[b] = (int32_t)prefill_len[b];
+    pl[b] = pb[b] = (int32_t)prefill_len[b];
     sb[b] = s->slot_base[(size_t)b];
     tb[b + 1] = tb[b] + prefill_len[b];
     tl[b + 1] = tl[b] + (int32_t)((prefill_len[b] + kPrefillTile - 1) / kPrefillTile);
@@ -425,6 +432,8 @@ rswa_status rswa_state_create_pooled(const rswa_config *cfg, const int64_t *pref
   v.rope = RSWA_ROPE_NONE;
   v.rope_theta = 10000.f;
   v.rope_cs = (float2 *)(w + s->ws.rope_cs);
+  v.pos_base = (int32_t *)(w + s->ws.pos_base);
+  v.ring_ml = (float2 *)(w + s->ws.ring_ml);
   v.total_tokens = tb[B];
   v.total_tiles = tl[B];
   v.total_tiles64 = tl64[B];

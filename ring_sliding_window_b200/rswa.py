@@ -25,6 +25,8 @@ _LIB_PATH = os.environ.get("RSWA_LIBRARY") or os.path.join(_PKG, "librswa.so")
 RSWA_OK, RSWA_EINVAL, RSWA_ENOMEM, RSWA_ECUDA, RSWA_ESTATE, RSWA_ETIMEOUT, RSWA_EDEVICE = range(7)
 RSWA_F32, RSWA_BF16 = 0, 1
 RSWA_DEVERR_TIMEOUT, RSWA_DEVERR_BAD_TOKEN, RSWA_DEVERR_BAD_LENGTH = 1, 2, 4
+RSWA_DEVERR_BAD_TREE = 8
+RSWA_TREE_MAX = 128
 
 EXPORTED = (
     "rswa_cache_bytes", "rswa_workspace_bytes", "rswa_state_create", "rswa_state_destroy",
@@ -35,7 +37,9 @@ EXPORTED = (
     "rswa_pool_free", "rswa_pool_stats", "rswa_pool_capacity", "rswa_pool_cache_bytes",
     "rswa_state_create_pooled", "rswa_ngram_topk", "rswa_state_set_rope",
     "rswa_state_set_attention", "rswa_decode_step_partial", "rswa_combine_partials",
-    "rswa_debug_prefill_plan",
+    "rswa_debug_prefill_plan", "rswa_tree_workspace_bytes", "rswa_tree_create",
+    "rswa_tree_destroy", "rswa_tree_set", "rswa_tree_attention", "rswa_tree_commit",
+    "rswa_tree_advance", "rswa_score_bytes", "rswa_decode_step_scored", "rswa_evict",
 )
 RSWA_ATTN_RING, RSWA_ATTN_STANDARD_SWA = 0, 1
 RSWA_ROPE_NONE, RSWA_ROPE_ABSOLUTE, RSWA_ROPE_SLOT = 0, 1, 2
@@ -116,6 +120,20 @@ lib.rswa_debug_inject_fault.argtypes = [_vp, ctypes.c_int32, _vp]
 lib.rswa_debug_inject_fault.restype = ctypes.c_int
 lib.rswa_debug_prefill_plan.argtypes = [_vp, _vp, ctypes.c_int32, _vp, ctypes.c_int64]
 lib.rswa_debug_prefill_plan.restype = ctypes.c_int64
+lib.rswa_tree_workspace_bytes.argtypes = [_vp, ctypes.c_int32]
+lib.rswa_tree_workspace_bytes.restype = ctypes.c_size_t
+lib.rswa_tree_create.argtypes = [_vp, ctypes.c_int32, _vp, ctypes.c_size_t, _vp,
+                                 ctypes.POINTER(_vp)]
+lib.rswa_tree_destroy.argtypes = [_vp]
+lib.rswa_tree_set.argtypes = [_vp, _vp, _vp, _vp]
+lib.rswa_tree_attention.argtypes = [_vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp]
+lib.rswa_tree_commit.argtypes = [_vp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp, _vp, _vp]
+lib.rswa_tree_advance.argtypes = [_vp, _vp]
+lib.rswa_score_bytes.argtypes = [_vp]
+lib.rswa_score_bytes.restype = ctypes.c_size_t
+lib.rswa_decode_step_scored.argtypes = [_vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+lib.rswa_evict.argtypes = [_vp, _vp, ctypes.c_int32, _vp, ctypes.c_int32, ctypes.c_int32, _vp, _vp,
+                           _vp]
 lib.rswa_last_cuda_error.argtypes = []
 lib.rswa_last_cuda_error.restype = ctypes.c_char_p
 lib.rswa_status_string.argtypes = [ctypes.c_int]
@@ -125,7 +143,9 @@ for _n in ("rswa_state_create", "rswa_state_destroy", "rswa_prefill", "rswa_deco
            "rswa_check_device_error", "rswa_decode_launch_shape", "rswa_pool_create",
            "rswa_pool_destroy", "rswa_pool_alloc", "rswa_pool_free", "rswa_pool_stats",
            "rswa_state_create_pooled", "rswa_ngram_topk", "rswa_state_set_rope",
-           "rswa_state_set_attention", "rswa_decode_step_partial", "rswa_combine_partials"):
+           "rswa_state_set_attention", "rswa_decode_step_partial", "rswa_combine_partials",
+           "rswa_tree_create", "rswa_tree_destroy", "rswa_tree_set", "rswa_tree_attention",
+           "rswa_tree_commit", "rswa_tree_advance", "rswa_decode_step_scored", "rswa_evict"):
     getattr(lib, _n).restype = ctypes.c_int
 
 
@@ -335,6 +355,63 @@ def rswa_combine_partials(part_ml, part_o, out, stream=None) -> None:
                                      _stream(stream)), "rswa_combine_partials")
 
 
+def rswa_tree_workspace_bytes(state, max_draft: int) -> int:
+    return int(lib.rswa_tree_workspace_bytes(state, int(max_draft)))
+
+
+def rswa_tree_create(state, max_draft: int, workspace, workspace_size, stream=None):
+    out = ctypes.c_void_p()
+    _check(lib.rswa_tree_create(state, int(max_draft), _ptr(workspace), int(workspace_size),
+                                _stream(stream), ctypes.byref(out)), "rswa_tree_create")
+    return out
+
+
+def rswa_tree_destroy(tree) -> None:
+    _check(lib.rswa_tree_destroy(tree), "rswa_tree_destroy")
+
+
+def rswa_tree_set(tree, parent, n_draft=None, stream=None) -> None:
+    """parent: cuda int32 [B, T] or None (chains); n_draft: cuda int32 [B] or None (all T)."""
+    _check(lib.rswa_tree_set(tree, _ptr(parent), _ptr(n_draft), _stream(stream)), "rswa_tree_set")
+
+
+def rswa_tree_attention(tree, layer, q, k_draft, v_draft, out, stream=None) -> None:
+    """q, k_draft, v_draft, out: [B, T, H, d]."""
+    _check(lib.rswa_tree_attention(tree, layer, _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(out),
+                                   _stream(stream)), "rswa_tree_attention")
+
+
+def rswa_tree_commit(tree, k_draft, v_draft, path, path_len, stream=None) -> None:
+    """k_draft, v_draft: one tensor a layer; path: cuda int32 [B, T]; path_len: cuda int32 [B]."""
+    kp = (ctypes.c_void_p * len(k_draft))(*[_ptr(t).value for t in k_draft])
+    vp = (ctypes.c_void_p * len(v_draft))(*[_ptr(t).value for t in v_draft])
+    _check(lib.rswa_tree_commit(tree, kp, vp, _ptr(path), _ptr(path_len), _stream(stream)),
+           "rswa_tree_commit")
+
+
+def rswa_tree_advance(tree, stream=None) -> None:
+    _check(lib.rswa_tree_advance(tree, _stream(stream)), "rswa_tree_advance")
+
+
+def rswa_score_bytes(state) -> int:
+    return int(lib.rswa_score_bytes(state))
+
+
+def rswa_decode_step_scored(state, layer, q, k_new, v_new, out, score_in, score_out, scratch,
+                            stream=None) -> None:
+    """rswa_decode_step, and score_out = score_in + softmax weight per cache entry
+    (float32 buffers of rswa_score_bytes)."""
+    _check(lib.rswa_decode_step_scored(state, layer, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out),
+                                       _ptr(score_in), _ptr(score_out), _ptr(scratch),
+                                       _stream(stream)), "rswa_decode_step_scored")
+
+
+def rswa_evict(src, dst, layer, score, n_first, n_last, dst_score, kept, stream=None) -> None:
+    """Keep the prompt entries with the highest scores of one layer of src in dst."""
+    _check(lib.rswa_evict(src, dst, layer, _ptr(score), int(n_first), int(n_last),
+                          _ptr(dst_score), _ptr(kept), _stream(stream)), "rswa_evict")
+
+
 def rswa_decode_launch_shape(state):
     """(grid, cluster_size) of this state's decode launches; cluster_size 0 = stream-K split."""
     g, c = ctypes.c_int32(0), ctypes.c_int32(0)
@@ -378,6 +455,16 @@ def rswa_debug_inject_fault(state, flags: int, stream=None) -> None:
     """Test-only: make this state's decode kernels drop their copies (their
     bounded waits then run out and report RSWA_ETIMEOUT); 0 restores."""
     _check(lib.rswa_debug_inject_fault(state, int(flags), _stream(stream)), "rswa_debug_inject_fault")
+
+
+# --------------------------------------------------------- argument checks
+def _require(t, what: str, shape, dtype, device) -> None:
+    """The C calls take bare pointers: a tensor of another type, shape, layout or
+    device would be read as if it had these."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
+            not t.is_contiguous() or t.device != device:
+        raise RswaError(RSWA_EINVAL, f"{what}: needs a contiguous {dtype} tensor "
+                                     f"{tuple(shape)} on {device}")
 
 
 # ---------------------------------------------------------- owning helper
@@ -461,6 +548,105 @@ class State:
                             stream=None):
         rswa_decode_step_partial(self.handle, layer, q, k_new, v_new, key_lo, key_hi, part_ml,
                                  part_o, stream)
+
+
+    def tree(self, max_draft: int, stream=None) -> "Tree":
+        """Trees of up to max_draft drafted tokens a sequence over this state."""
+        return Tree(self, max_draft, stream)
+
+    @property
+    def _device(self):
+        return self.workspace.device
+
+    def score_buffer(self) -> torch.Tensor:
+        """A layer's accumulated attention weights, all zero."""
+        return torch.zeros(rswa_score_bytes(self.handle) // 4, dtype=torch.float32,
+                           device=self._device)
+
+    def score_view(self, score: torch.Tensor, b: int, h: int) -> torch.Tensor:
+        """[P_b + W] view of one (b, h) ring of a score buffer."""
+        off = rswa_cache_offset(self.handle, b, h, 0) // self.d
+        return score[off:off + self.prefill_lens[b] + self.W]
+
+    def decode_step_scored(self, layer, q, k_new, v_new, out, score_in, score_out, scratch,
+                           stream=None):
+        for t, what in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (out, "out")):
+            _require(t, what, (self.B, self.H, self.d), self.dtype, self._device)
+        n = rswa_score_bytes(self.handle) // 4
+        for t, what in ((score_in, "score_in"), (score_out, "score_out"), (scratch, "scratch")):
+            _require(t, what, (n,), torch.float32, self._device)
+        rswa_decode_step_scored(self.handle, layer, q, k_new, v_new, out, score_in, score_out,
+                                scratch, stream)
+
+    def evict_into(self, dst: "State", layer, score, n_first: int = 0, n_last: int = 0,
+                   dst_score=None, kept=None, stream=None) -> torch.Tensor:
+        """Keep dst.prefill_lens prompt entries a ring of this layer, by score, in
+        `dst`.  Returns the kept source slots (int32 [H * sum P'])."""
+        if kept is None:
+            kept = torch.empty(self.H * sum(dst.prefill_lens), dtype=torch.int32,
+                               device=self._device)
+        _require(kept, "kept", (self.H * sum(dst.prefill_lens),), torch.int32, self._device)
+        _require(score, "score", (rswa_score_bytes(self.handle) // 4,), torch.float32,
+                 self._device)
+        if dst_score is not None:
+            _require(dst_score, "dst_score", (rswa_score_bytes(dst.handle) // 4,), torch.float32,
+                     self._device)
+        rswa_evict(self.handle, dst.handle, layer, score, n_first, n_last, dst_score, kept, stream)
+        return kept
+
+
+class Tree:
+    """Trees of drafted tokens over a State: the workspace (torch-allocated) and
+    its rswa_tree."""
+
+    def __init__(self, state: State, max_draft: int, stream=None):
+        self.state, self.T = state, int(max_draft)
+        wb = rswa_tree_workspace_bytes(state.handle, self.T)
+        if wb == 0:
+            raise RswaError(RSWA_EINVAL, "rswa_tree_workspace_bytes")
+        self.workspace = torch.empty(wb, dtype=torch.uint8, device=state.workspace.device)
+        self.handle = rswa_tree_create(state.handle, self.T, self.workspace, wb, stream)
+
+    def _drafts(self, t, what):
+        st = self.state
+        _require(t, what, (st.B, self.T, st.H, st.d), st.dtype, st._device)
+
+    def set(self, parent=None, n_draft=None, stream=None):
+        st = self.state
+        if parent is not None:
+            _require(parent, "parent", (st.B, self.T), torch.int32, st._device)
+        if n_draft is not None:
+            _require(n_draft, "n_draft", (st.B,), torch.int32, st._device)
+        rswa_tree_set(self.handle, parent, n_draft, stream)
+
+    def attention(self, layer, q, k_draft, v_draft, out, stream=None):
+        for t, what in ((q, "q"), (k_draft, "k_draft"), (v_draft, "v_draft"), (out, "out")):
+            self._drafts(t, what)
+        rswa_tree_attention(self.handle, layer, q, k_draft, v_draft, out, stream)
+
+    def commit(self, k_draft, v_draft, path, path_len, stream=None):
+        st = self.state
+        if len(k_draft) != st.L or len(v_draft) != st.L:
+            raise RswaError(RSWA_EINVAL, "commit: needs one k_draft and one v_draft a layer")
+        for t in (*k_draft, *v_draft):
+            self._drafts(t, "draft")
+        _require(path, "path", (st.B, self.T), torch.int32, st._device)
+        _require(path_len, "path_len", (st.B,), torch.int32, st._device)
+        rswa_tree_commit(self.handle, k_draft, v_draft, path, path_len, stream)
+
+    def advance(self, stream=None):
+        rswa_tree_advance(self.handle, stream)
+
+    def close(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            rswa_tree_destroy(h)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class TokenPool:

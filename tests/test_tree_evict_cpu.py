@@ -1,0 +1,46 @@
+"""Host-side checks of the draft-tree and eviction calls: refused before anything is
+launched, on any machine."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def rswa():
+    from ring_sliding_window_b200 import build
+    build.build()
+    from ring_sliding_window_b200 import rswa as mod
+    return mod
+
+
+A = 4096  # an aligned stand-in address, never dereferenced on these paths
+
+
+def test_null_objects_are_refused(rswa):
+    lib, E = rswa.lib, rswa.RSWA_EINVAL
+    out = rswa.ctypes.c_void_p()
+    assert lib.rswa_tree_workspace_bytes(None, 8) == 0
+    assert lib.rswa_tree_create(None, 8, A, 1 << 20, None, rswa.ctypes.byref(out)) == E
+    assert lib.rswa_tree_create(None, 8, A, 1 << 20, None, None) == E
+    assert lib.rswa_tree_destroy(None) == E
+    assert lib.rswa_tree_set(None, None, None, None) == E
+    assert lib.rswa_tree_attention(None, 0, A, A, A, A, None) == E
+    assert lib.rswa_tree_commit(None, None, None, A, A, None) == E
+    assert lib.rswa_tree_advance(None, None) == E
+    assert lib.rswa_score_bytes(None) == 0
+    assert lib.rswa_decode_step_scored(None, 0, A, A, A, A, A, A, A, None) == E
+    assert lib.rswa_evict(None, None, 0, A, 0, 0, A, A, None) == E
+
+
+def test_reference_kept_slots():
+    """The tests' own definition, on a hand-made case."""
+    import tree_reference as ref
+    nan = float("nan")
+    assert ref.kept_slots([1, 3, 3, 2, nan, 0], 2, 0, 0) == [1, 2]
+    assert ref.kept_slots([1, 3, 3, 2, nan, 0], 3, 1, 1) == [0, 1, 5]
+    assert ref.kept_slots([0.0, -0.0, nan], 1, 0, 0) == [0]
+    assert ref.kept_slots([nan, 0.0], 1, 0, 0) == [1]
+
+
+def test_reference_paths():
+    import tree_reference as ref
+    assert ref.path_of([-1, 0, 0, 2], 3) == [0, 2, 3]
+    assert ref.path_of([-1, -1], 1) == [1]

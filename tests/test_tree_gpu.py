@@ -1,0 +1,438 @@
+"""Attention of drafted trees over the ring cache, commit and advance, against the
+definition in 64 bits and against ordinary decode steps."""
+import numpy as np
+import pytest
+import torch
+
+import tree_reference as ref
+from helpers import f64, tol_for
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _rswa():
+    from ring_sliding_window_b200 import rswa
+    return rswa
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Case:
+    def __init__(self, dtype, d, H, W, plens, t, T, n=None, parents=None, seed=1, layers=1,
+                 scale=0.0, tail=None):
+        rswa = _rswa()
+        self.B, self.T, self.H, self.d, self.W = len(plens), T, H, d, W
+        self.model = ref.Model(plens, W, H, d, dtype, seed).generate(t)
+        self.st = rswa.State(self.B, layers, H, d, W, plens, dtype=dtype, n_generated=t,
+                             scale=scale)
+        for layer in range(layers):
+            self.model.fill(self.st, layer)
+        rng = np.random.default_rng(seed)
+        self.n = [T] * self.B if n is None else list(n)
+        self.parents = [ref.random_parents(rng, T) for _ in plens] if parents is None else parents
+        self.q, self.k, self.v = (self.model.draw(self.B, T, H, d) for _ in range(3))
+        self.scale = scale or d ** -0.5
+        self.tree = self.st.tree(T)
+
+    def run(self, layer=0):
+        out = torch.full((self.B, self.T, self.H, self.d), 7.0, dtype=self.model.dtype,
+                         device="cuda")
+        self.tree.set(_ints(self.parents), _ints(self.n))
+        self.tree.attention(layer, self.q.cuda(), self.k.cuda(), self.v.cuda(), out)
+        torch.cuda.synchronize()
+        assert self.st.check() == 0
+        return out.cpu()
+
+    def check(self, out, swa=False, rows=None):
+        m = self.model
+        for b in range(self.B):
+            for i in range(self.T):
+                if i >= self.n[b]:
+                    assert bool((out[b, i] == 7.0).all()), "a row that holds no draft was written"
+                    continue
+                if rows is not None and i not in rows:
+                    continue
+                path = ref.path_of(self.parents[b], i)
+                for h in range(self.H):
+                    k, v = m.entries(b, h, [self.k[b, x] for x in path],
+                                     [self.v[b, x] for x in path], swa)
+                    o, mass = ref.attend(self.q[b, i, h], k, v, self.scale)
+                    err = (out[b, i, h].double() - o).abs()
+                    lim = ref.tolerance(o, mass, m.dtype)
+                    assert bool((err <= lim).all()), (b, i, h, float((err / lim).max()))
+
+
+KINDS = [(BF, 128), (BF, 64), (F32, 128), (F32, 64)]
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("T,W,plens,t", [
+    (1, 8, (5,), (0,)),                    # one draft, nothing generated yet
+    (1, 128, (1088,), (500,)),
+    (4, 1, (3, 0), (2, 1)),                # the window holds the draft alone
+    (8, 8, (0, 1, 130), (3, 8, 9)),        # no prompt; rings part full, full, wrapped
+    (17, 5, (100, 64), (4, 23)),           # paths deeper than the window
+    (33, 128, (257, 63, 128), (127, 128, 300)),
+    (64, 100, (200,), (37,)),
+    (65, 40, (190, 7), (55, 41)),
+    (128, 129, (255,), (260,)),
+    (128, 16, (65,), (10,)),
+])
+def test_tree_matches_the_definition(dtype, d, T, W, plens, t):
+    rng = np.random.default_rng(T)
+    n = [T] + [int(rng.integers(0, T + 1)) for _ in plens[1:]]
+    c = Case(dtype, d, 2, W, plens, t, T, n=n)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("parents", ["chain", "star", "pairs"])
+def test_tree_shapes(dtype, d, parents):
+    T = 40
+    p = {"chain": [i - 1 for i in range(T)], "star": [-1] * T,
+         "pairs": [(i - 1) // 2 if i else -1 for i in range(T)]}[parents]
+    c = Case(dtype, d, 3, 24, (150, 31), (30, 5), T, parents=[p, p])
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_tree_over_many_tiles_and_pieces(dtype, d):
+    """Long prompts: rings split over several CTAs, CTAs holding parts of several rings."""
+    c = Case(dtype, d, 2, 128, (5000, 17, 1300), (700, 3, 128), 24, n=(24, 9, 0))
+    c.check(c.run(), rows=(0, 3, 8, 23))
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_tree_with_more_rings_than_ctas(dtype, d):
+    B = 90
+    plens = tuple(int(x) for x in np.random.default_rng(3).integers(0, 300, B))
+    t = tuple(int(x) for x in np.random.default_rng(4).integers(0, 40, B))
+    n = [int(x) for x in np.random.default_rng(5).integers(0, 12, B)]
+    c = Case(dtype, d, 4, 16, plens, t, 11, n=n)
+    c.check(c.run(), rows=(0, 5, 10))
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_values_a_draft_does_not_see_never_reach_it(dtype, d, bad):
+    """Non-finite keys and values in a sibling branch, in a ring entry that deeper drafts have
+    outlived, and in rows behind the last draft: only the drafts that see them change."""
+    T, W, P = 12, 10, 140
+    parents = [[-1, 0, 1, 2, -1, 4, 5, 6, 7, 8, 9, 10]]
+    c = Case(dtype, d, 2, W, (P,), (25,), T, n=(T - 1,), parents=parents, seed=5)
+    clean = c.run()
+    c.check(clean)
+    # draft 4 and its branch (4..10) hold the bad value; drafts 0..3 do not see it
+    c.k[0, 4, :, 3] = bad
+    c.v[0, 4, :, 5] = bad
+    c.v[0, T - 1] = bad
+    c.k[0, T - 1] = bad
+    out = c.run()
+    assert torch.equal(out[:, :4], clean[:, :4])
+    assert not bool(torch.isfinite(out[0, 5, :, 5]).any())
+    # token 15 (slot P + 25 mod 10, which token 25 would overwrite): seen by no draft
+    c = Case(dtype, d, 2, W, (P,), (25,), T, parents=parents, seed=6)
+    clean = c.run()
+    for h in range(2):
+        c.st.cache_view(0, "v", 0, h)[P + 5, 7] = bad
+        c.st.cache_view(0, "k", 0, h)[P + 5, 9] = bad
+    assert torch.equal(c.run(), clean)
+    # token 16, the oldest that a draft at depth 0 (token 25) sees; deeper ones do not
+    for h in range(2):
+        c.st.cache_view(0, "v", 0, h)[P + 6, 7] = bad
+    out = c.run()
+    shallow = [0, 4]
+    deep = [i for i in range(T) if i not in shallow]
+    assert torch.equal(out[:, deep], clean[:, deep])
+    # the drafts that see it: that element alone takes the value on
+    assert not bool(torch.isfinite(out[0, shallow, :, 7]).any())
+    others = [e for e in range(d) if e != 7]
+    assert torch.equal(out[:, shallow][..., others], clean[:, shallow][..., others])
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_large_scores(dtype, d):
+    """Scores of hundreds, growing along the keys: the running maximum moves at every tile."""
+    c = Case(dtype, d, 2, 16, (700,), (20,), 9, seed=8)
+    m = c.model
+    ramp = torch.linspace(0, 40, 700)[:, None, None]
+    m.pk[0] = (m.pk[0].float() * 0.05 + ramp * torch.sign(c.q[0, 0].float()) / d ** 0.5).to(dtype)
+    m.fill(c.st)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("rope", [0, 1, 2])
+@pytest.mark.parametrize("swa", [False, True])
+def test_chain_verify_and_commit_equals_decode_steps(dtype, d, rope, swa):
+    """A chain of drafts gives what as many decode steps give, layer by layer, and after the
+    commit the caches, counters and next step are the same: across ring wraps."""
+    rswa = _rswa()
+    B, L, H, W, plens, T = 2, 2, 3, 12, (150, 20), 9
+    a, b = (rswa.State(B, L, H, d, W, plens, dtype=dtype) for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def draw(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+    for st in (a, b):
+        if rope:
+            st.set_rope(rope)
+        if swa:
+            st.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)
+    tot = sum(plens)
+    for layer in range(L):
+        q, k, v = (draw(tot, H, d) for _ in range(3))
+        for st in (a, b):
+            st.prefill(layer, q, k, v, torch.empty_like(q))
+    tree = b.tree(T)
+    # two roundings of a weight and of the output on either side; rope rounds q on the tree's
+    tol = (2e-2 if dtype == BF else 1e-5)
+    for step in range(4):
+        qs, ks, vs = ([draw(B, T, H, d) for _ in range(L)] for _ in range(3))
+        tree.set()
+        outs = [torch.empty(B, T, H, d, dtype=dtype, device="cuda") for _ in range(L)]
+        for layer in range(L):
+            tree.attention(layer, qs[layer], ks[layer], vs[layer], outs[layer])
+        take = (T, 4)
+        path = torch.arange(T, dtype=torch.int32, device="cuda").repeat(B, 1)
+        tree.commit(ks, vs, path, _ints(take))
+        tree.advance()
+        for i in range(T):
+            for layer in range(L):
+                o = torch.empty(B, H, d, dtype=dtype, device="cuda")
+                a.decode_step(layer, qs[layer][:, i].contiguous(), ks[layer][:, i].contiguous(),
+                              vs[layer][:, i].contiguous(), o)
+                for r in range(B):
+                    err = float((o[r].double() - outs[layer][r, i].double()).abs().max())
+                    assert i >= take[r] or err <= tol, (step, i, layer, r, err)
+            a.advance()
+            if i == 3:  # the second sequence stops here: keep its rings and counter
+                saved = [[(a.cache_view(layer, w, 1, h).clone(), layer, w, h) for h in range(H)]
+                         for layer in range(L) for w in "kv"]
+                t_saved = a.ring()[0][1]
+        # sequence 0 took all T; sequence 1 took 4: compare each with the decode path
+        for layer in range(L):
+            for h in range(H):
+                for w in "kv":
+                    x, y = a.cache_view(layer, w, 0, h), b.cache_view(layer, w, 0, h)
+                    held = plens[0] + min(a.ring()[0][0], W)
+                    assert torch.equal(x[:held], y[:held])
+        for group in saved:
+            for x, layer, w, h in group:
+                held = plens[1] + min(t_saved, W)
+                assert torch.equal(x[:held], b.cache_view(layer, w, 1, h)[:held])
+                a.cache_view(layer, w, 1, h).copy_(b.cache_view(layer, w, 1, h))
+        assert b.ring()[0][0] == a.ring()[0][0] and b.ring()[0][1] == t_saved
+        # rebuild the decode side at the tree side's counters for the next step
+        na = rswa.State(B, L, H, d, W, plens, dtype=dtype, n_generated=b.ring()[0])
+        for layer in range(L):
+            na.k_cache[layer].copy_(b.k_cache[layer])
+            na.v_cache[layer].copy_(b.v_cache[layer])
+        if rope:
+            na.set_rope(rope)
+        if swa:
+            na.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)
+        a = na
+    assert a.check() == 0 and b.check() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_standard_window_matches_the_definition(dtype, d):
+    rswa = _rswa()
+    c = Case(dtype, d, 2, 70, (300, 40, 71), (20, 90, 0), 13)
+    c.st.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)
+    c.check(c.run(), swa=True)
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_commit_writes_the_path_and_nothing_else(dtype, d):
+    L, H, W, plens, t, T = 3, 2, 6, (5, 9, 0, 4), (2, 11, 6, 30), 10
+    c = Case(dtype, d, H, W, plens, t, T, layers=L)
+    c.parents = [[i - 1 for i in range(T)], [-1, -1, 0, 2, 1, 4, 5, 5, 7, 8], [-1] * T,
+                 [i - 1 for i in range(T)]]
+    paths = [[0, 1, 2], [1, 4, 5, 7, 8, 9], [], list(range(T))]  # the last is longer than W
+    before = [[x.clone() for x in c.st.k_cache], [x.clone() for x in c.st.v_cache]]
+    ks, vs = ([c.model.draw(len(plens), T, H, d).cuda() for _ in range(L)] for _ in range(2))
+    path = torch.zeros(len(plens), T, dtype=torch.int32)
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = torch.tensor(p, dtype=torch.int32)
+    c.tree.set(_ints(c.parents))
+    c.tree.commit(ks, vs, path.cuda(), _ints([len(p) for p in paths]))
+    base = 0
+    for b, p in enumerate(paths):
+        size = plens[b] + W
+        for i, node in list(enumerate(p)):
+            for layer in range(L):
+                for h in range(H):
+                    row = base * H + h * size + plens[b] + (t[b] + i) % W
+                    for buf, src in ((before[0], ks), (before[1], vs)):
+                        buf[layer].view(-1, d)[row] = src[layer][b, node, h]
+        base += size
+    same = [torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+            for x, y in zip(c.st.k_cache + c.st.v_cache, before[0] + before[1])]
+    assert all(same)
+    assert c.st.ring()[0] == list(t)
+    c.tree.advance()
+    assert c.st.ring()[0] == [x + len(p) for x, p in zip(t, paths)]
+    c.tree.advance()  # counted once
+    assert c.st.ring()[0] == [x + len(p) for x, p in zip(t, paths)]
+    assert c.st.check() == 0
+
+
+def test_bad_trees_and_paths_are_refused_sequence_by_sequence():
+    rswa = _rswa()
+    T, W = 6, 8
+    c = Case(BF, 128, 2, W, (20, 20, 20, 20, 20), (3, 3, 3, 3, 3), T)
+    good = [-1, 0, 1, 1, 3, 0]
+    # own parent, a later parent, below -1, a count above T
+    c.parents = [good, [-1, 1, 0, 0, 0, 0], [-1, 0, 5, 0, 0, 0], [-2, 0, 0, 0, 0, 0], good]
+    c.tree.set(_ints(c.parents), _ints([T, T, T, T, T + 1]))
+    out = torch.full((5, T, 2, 128), 7.0, dtype=BF, device="cuda")
+    c.tree.attention(0, c.q.cuda(), c.k.cuda(), c.v.cuda(), out)
+    assert c.st.check() == rswa.RSWA_EDEVICE
+    assert c.st.check() == 0
+    assert bool((out[1:] == 7.0).all()) and bool((out[0] != 7.0).any())
+    # paths: not a chain, not from a first node, a node out of range, too long, of a refused tree
+    c.tree.set(_ints([good] * 5), _ints([T, T, T, T, 4]))
+    before = [x.clone() for x in c.st.k_cache + c.st.v_cache]
+    paths = [[0, 1, 4, 0, 0, 0], [1, 3, 0, 0, 0, 0], [0, 6, 0, 0, 0, 0], [0] * T, [0, 1, 3, 4, 0, 0]]
+    c.tree.commit([c.k.cuda()], [c.v.cuda()], _ints(paths), _ints([3, 2, 2, T + 1, 4]))
+    assert c.st.check() == rswa.RSWA_EDEVICE
+    for x, y in zip(before, c.st.k_cache + c.st.v_cache):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    c.tree.advance()
+    assert c.st.ring()[0] == [3] * 5
+    # padding behind the drafts is not looked at
+    c.tree.set(_ints([good[:3] + [99, -7, 5]] * 5), _ints([3] * 5))
+    assert c.st.check() == 0
+
+
+def test_tree_step_in_a_graph():
+    """set, attention, commit and advance captured once and replayed over new inputs."""
+    T, W, L, H, d, plens, t = 5, 7, 2, 2, 128, (140, 30), (4, 9)
+    c, e = (Case(BF, d, H, W, plens, t, T, layers=L, seed=9) for _ in range(2))
+    static = {"parent": _ints(c.parents), "n": _ints([T, T]), "path": _ints([[0] * T] * 2),
+              "len": _ints([0, 0])}
+    qs, ks, vs = ([torch.zeros(2, T, H, d, dtype=BF, device="cuda") for _ in range(L)]
+                  for _ in range(3))
+    outs = [torch.zeros_like(x) for x in qs]
+
+    def step(x):
+        x.tree.set(static["parent"], static["n"])
+        for layer in range(L):
+            x.tree.attention(layer, qs[layer], ks[layer], vs[layer], outs[layer])
+        x.tree.commit(ks, vs, static["path"], static["len"])
+        x.tree.advance()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(c)  # warm-up on zeros: nothing accepted
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(c)
+    rng = np.random.default_rng(2)
+    for _ in range(5):
+        parents = [ref.random_parents(rng, T) for _ in range(2)]
+        paths = [ref.path_of(p, int(rng.integers(0, T))) for p in parents]
+        static["parent"].copy_(_ints(parents))
+        static["path"].copy_(_ints([p + [0] * (T - len(p)) for p in paths]))
+        static["len"].copy_(_ints([len(p) for p in paths]))
+        for x in qs + ks + vs:
+            x.copy_(c.model.draw(2, T, H, d))
+        graph.replay()
+        got = [x.clone() for x in outs]
+        step(e)
+        for x, y in zip(got, outs):
+            assert torch.equal(x, y)
+        for x, y in zip(c.st.k_cache + c.st.v_cache, e.st.k_cache + e.st.v_cache):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+        assert c.st.ring() == e.st.ring()
+    assert c.st.check() == 0 and e.st.check() == 0
+
+
+def test_two_trees_on_two_streams():
+    """Two states, each with its tree, stepped at the same time on streams of their own."""
+    cases = [Case(BF, 128, 4, 64, (3000, 500), (70, 9), 31, seed=s) for s in (21, 22)]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    ins = [(c.q.cuda(), c.k.cuda(), c.v.cuda(), _ints(c.parents)) for c in cases]
+    outs = [torch.full_like(i[0], 7.0) for i in ins]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, s, i, o in zip(cases, streams, ins, outs):
+            c.tree.set(i[3], None, stream=s)
+            c.tree.attention(0, i[0], i[1], i[2], o, stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert torch.equal(w, o.cpu())
+
+
+def test_repeats_are_equal_bit_for_bit():
+    c = Case(BF, 128, 3, 128, (4000, 300), (200, 50), 47)
+    first = c.run()
+    for _ in range(3):
+        assert torch.equal(first, c.run())
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_tree_over_a_pool(dtype, d):
+    """Requests placed anywhere in a pool, other requests' slots holding NaN."""
+    rswa = _rswa()
+    H, W, plens, t, T = 2, 9, (33, 140), (4, 12), 6
+    pool = rswa.TokenPool(600, 1, H, d, W, dtype=dtype)
+    pool.k_cache[0].fill_(float("nan"))
+    pool.v_cache[0].fill_(float("nan"))
+    pool.alloc(50)
+    bases = [pool.alloc(p) for p in plens][::-1]
+    bases = [pool.alloc(plens[0]), bases[0]]
+    c = Case(dtype, d, H, W, plens, t, T)
+    st = pool.state(plens, bases, n_generated=t)
+    c.model.fill(st)
+    c.st, c.tree = st, st.tree(T)
+    c.check(c.run())
+
+
+def test_refusals():
+    rswa = _rswa()
+    c = Case(BF, 128, 2, 8, (20,), (3,), 4)
+    q, k, v = c.q.cuda(), c.k.cuda(), c.v.cuda()
+    out = torch.empty_like(q)
+    for T in (0, -1, rswa.RSWA_TREE_MAX + 1):
+        with pytest.raises(rswa.RswaError):
+            c.st.tree(T)
+    with pytest.raises(rswa.RswaError) as e:
+        rswa.rswa_tree_create(c.st.handle, 4, c.tree.workspace, 16)
+    assert e.value.status == rswa.RSWA_ENOMEM
+    bad = [(1, q, k, v, out), (-1, q, k, v, out), (0, q[:, :2], k, v, out),
+           (0, q.float(), k, v, out), (0, q.cpu(), k, v, out),
+           (0, q.transpose(1, 2).contiguous().transpose(1, 2), k, v, out)]
+    for args in bad:
+        with pytest.raises(rswa.RswaError) as e:
+            c.tree.attention(*args)
+        assert e.value.status == rswa.RSWA_EINVAL
+    with pytest.raises(rswa.RswaError):
+        rswa.rswa_tree_attention(c.tree.handle, 0, q.data_ptr() + 2, k, v, out)
+    with pytest.raises(rswa.RswaError):
+        c.tree.set(torch.zeros(1, 4, dtype=torch.int64, device="cuda"))
+    with pytest.raises(rswa.RswaError):
+        c.tree.commit([k, k], [v, v], _ints([[0] * 4]), _ints([1]))
+    fresh = rswa.State(1, 1, 2, 128, 8, [20], dtype=BF)
+    tree = fresh.tree(4)
+    tree.set()
+    with pytest.raises(rswa.RswaError) as e:
+        tree.attention(0, q, k, v, out)
+    assert e.value.status == rswa.RSWA_ESTATE
+    with pytest.raises(rswa.RswaError) as e:
+        tree.commit([k], [v], _ints([[0] * 4]), _ints([1]))
+    assert e.value.status == rswa.RSWA_ESTATE
+    # before any rswa_tree_set nothing is drafted
+    out.fill_(7.0)
+    c.tree.attention(0, q, k, v, out)
+    assert bool((out == 7.0).all())
