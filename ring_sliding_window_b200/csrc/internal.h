@@ -1,6 +1,7 @@
 // Internal declarations shared by the librswa host layer and its kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -61,6 +62,8 @@ struct DecodePlan {
 constexpr int kTopkMax = 64;                 // largest k of rswa_ngram_topk
 constexpr int kTopkMaxVocab = 16 * 16384;    // 16 CTAs of 16,384 columns per row
 constexpr int kTopkMaxWindow = 8192;         // history staged in shared memory
+constexpr int kTreeTcTile = 128;    // keys per tile of the tensor-core tree kernel
+constexpr int kTreeSimtTile = 64;   // keys per tile of the FP32 tree kernel
 constexpr int kPrefillTile = 128;  // query rows per prefill tile (tensor-core kernel)
 constexpr int kSimtTile = 64;      // query rows per prefill tile (FP32 SIMT kernel)
 
@@ -106,7 +109,6 @@ struct DeviceView {
 // A tree of drafted tokens per sequence, as the kernels see it.
 struct TreeView {
   int T;                     // drafted tokens a sequence (the row stride of the inputs)
-  int tile;                  // keys a tile of the work plan holds
   int grid;                  // attention CTAs
   const DecodePiece *pieces; // key_begin / key_end count tiles: the drafts' first, then the cache's
   const int32_t *cta_piece;  // [grid + 1]
@@ -192,11 +194,18 @@ cudaError_t launch_tree_set(const DeviceView &v, const TreeView &tv, const int32
                             const int32_t *n_draft, cudaStream_t s);
 // (cos, sin) of every draft's position (RoPE; nothing to do without it).
 cudaError_t launch_tree_rope(const DeviceView &v, const TreeView &tv, cudaStream_t s);
-cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const void *q,
-                             const void *kd, const void *vd, const void *kc, const void *vc,
-                             void *out, cudaStream_t s);
-// CTAs of the tree attention kernel for (dtype, head_dim) that one SM holds.
-int tree_simt_ctas_per_sm(int dtype, int head_dim, int n_rows);
+cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const float *q,
+                             const float *kd, const float *vd, const float *kc, const float *vc,
+                             float *out, cudaStream_t s);
+// CTAs of the FP32 kernel that one SM holds.
+int tree_simt_ctas_per_sm(int head_dim, int n_rows);
+// The tensor-core form (bf16), and the tensor maps over one layer's caches that
+// it takes (cache_rows rows of d elements); false if they cannot be made.
+bool tree_tc_maps(const DeviceView &v, const void *kc, const void *vc, int64_t cache_rows,
+                  CUtensorMap *tkc, CUtensorMap *tvc);
+cudaError_t launch_tree_tc(const DeviceView &v, const TreeView &tv, const CUtensorMap &tkc,
+                           const CUtensorMap &tvc, const void *q, const void *kd, const void *vd,
+                           const void *vc, void *out, cudaStream_t s);
 // Merge of the pieces of every ring that has more than one.
 cudaError_t launch_tree_combine(const DeviceView &v, const TreeView &tv, void *out,
                                 cudaStream_t s);

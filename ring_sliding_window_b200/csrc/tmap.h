@@ -26,18 +26,24 @@ inline EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
-// [rows][H * 128] bf16 rows, boxes of 64 elements x box_rows rows, 128-byte
+// [rows][row_elems] bf16 rows, boxes of 64 elements x box_rows rows, 128-byte
 // swizzle (the K-major operand layout of the tensor-core MMAs).
-inline bool make_tmap_bf16(CUtensorMap *m, const void *base, int64_t rows, int H, int box_rows) {
+inline bool make_tmap_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t row_elems,
+                           int box_rows) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)H * 128, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)H * 128 * 2};
+  const cuuint64_t dims[2] = {(cuuint64_t)row_elems, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_elems * 2};
   const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same over [rows][H * 128].
+inline bool make_tmap_bf16(CUtensorMap *m, const void *base, int64_t rows, int H, int box_rows) {
+  return make_tmap_rows(m, base, rows, (int64_t)H * 128, box_rows);
 }
 
 }  // namespace rswa

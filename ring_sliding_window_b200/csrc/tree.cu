@@ -11,6 +11,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <memory>
 #include <new>
 #include <vector>
 
@@ -25,6 +26,7 @@ struct rswa_tree {
   rswa_state *state;
   TreeView tv;
   int n_pieces;
+  std::vector<CUtensorMap> tm_k, tm_v;  // every layer's caches (bf16)
 };
 
 namespace rswa {
@@ -268,11 +270,9 @@ DecodePlan plan_tree(const rswa_state *s, int T, int tile, int ctas) {
   return p;
 }
 
-constexpr int kSimtKeys = 64;  // keys of a plan tile of tree_simt_kernel
-
 DecodePlan plan_for(const rswa_state *s, int T) {
-  return plan_tree(s, T, kSimtKeys,
-                   s->num_sms * tree_simt_ctas_per_sm(s->cfg.dtype, s->cfg.head_dim, T));
+  if (s->cfg.dtype == RSWA_BF16) return plan_tree(s, T, kTreeTcTile, s->num_sms);
+  return plan_tree(s, T, kTreeSimtTile, s->num_sms * tree_simt_ctas_per_sm(s->cfg.head_dim, T));
 }
 
 struct TreeLayout {
@@ -371,13 +371,22 @@ rswa_status rswa_tree_create(rswa_state *state, int32_t max_draft, void *workspa
     cudaError_t e = cudaMemcpyAsync(workspace, img.data(), img.size(), cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return from_cuda(e);
-    rswa_tree *t = new rswa_tree();
+    std::unique_ptr<rswa_tree> t(new rswa_tree());
+    if (state->cfg.dtype == RSWA_BF16) {
+      const size_t L = (size_t)state->cfg.num_layers;
+      t->tm_k.resize(L);
+      t->tm_v.resize(L);
+      for (size_t l = 0; l < L; ++l)
+        if (!tree_tc_maps(state->dv, state->k_cache[l], state->v_cache[l],
+                          (int64_t)state->cfg.num_heads * state->pool_slots, &t->tm_k[l],
+                          &t->tm_v[l]))
+          return RSWA_EINVAL;
+    }
     uint8_t *base = (uint8_t *)workspace;
     t->state = state;
     t->n_pieces = p.n_pieces;
     TreeView &tv = t->tv;
     tv.T = max_draft;
-    tv.tile = kSimtKeys;
     tv.grid = p.grid;
     tv.pieces = (const DecodePiece *)(base + w.pieces);
     tv.cta_piece = (const int32_t *)(base + w.cta_piece);
@@ -390,7 +399,7 @@ rswa_status rswa_tree_create(rswa_state *state, int32_t max_draft, void *workspa
     tv.n = (int32_t *)(base + w.n);
     tv.accepted = (int32_t *)(base + w.accepted);
     tv.cs = (float2 *)(base + w.cs);
-    *out = t;
+    *out = t.release();
     return RSWA_OK;
   } catch (const std::exception &) {
     return RSWA_ENOMEM;
@@ -420,8 +429,14 @@ rswa_status rswa_tree_attention(rswa_tree *tree, int32_t layer, const void *q, c
   if (!s->layer_ready[(size_t)layer]) return RSWA_ESTATE;
   if (current_device() != s->device) return RSWA_EINVAL;
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = launch_tree_simt(s->dv, tree->tv, q, k_draft, v_draft, s->k_cache[(size_t)layer],
-                                   s->v_cache[(size_t)layer], out, st);
+  const size_t l = (size_t)layer;
+  cudaError_t e =
+      s->cfg.dtype == RSWA_BF16
+          ? launch_tree_tc(s->dv, tree->tv, tree->tm_k[l], tree->tm_v[l], q, k_draft, v_draft,
+                           s->v_cache[l], out, st)
+          : launch_tree_simt(s->dv, tree->tv, (const float *)q, (const float *)k_draft,
+                             (const float *)v_draft, (const float *)s->k_cache[l],
+                             (const float *)s->v_cache[l], (float *)out, st);
   if (e == cudaSuccess && tree->n_pieces > s->cfg.batch * s->cfg.num_heads)
     e = launch_tree_combine(s->dv, tree->tv, out, st);
   return from_cuda(e);

@@ -14,7 +14,6 @@
 // kRows / 16 query rows x 4 keys of the scores, then the same rows x D / 16
 // output columns.  Groups of 16 rows (fewer than 17 drafts) or 64.  Bound by
 // FP32 FMA issue once a row group is full.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -26,7 +25,7 @@ namespace rswa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kKeys = 64;
+constexpr int kKeys = kTreeSimtTile;
 constexpr int kThreads = 256;
 constexpr float kMasked = -1.f;  // marks an unseen pair where a weight (>= 0) would stand
 
@@ -45,19 +44,19 @@ struct SimtSmem {
 struct TreeSimtArgs {
   DeviceView v;
   TreeView tv;
-  const void *q, *kd, *vd, *kc, *vc;
-  void *out;
+  const float *q, *kd, *vd, *kc, *vc;
+  float *out;
 };
 
-// 16-byte chunk c of a row of D elements at `src` into floats at dst; with cs,
-// both halves' chunks c and c + D / (2 N) are turned (rotate-half RoPE).
-template <typename T, int D>
-__device__ __forceinline__ void load_rotated(const T *src, float *dst, int c, const float2 *cs,
-                                             bool round) {
-  constexpr int N = Chunk<T>::N;
+// Elements 4 c .. 4 c + 3 of both halves of the row at `src` into dst, turned by
+// the (cos, sin) table cs if there is one (rotate-half RoPE).
+template <int D>
+__device__ __forceinline__ void load_rotated(const float *src, float *dst, int c,
+                                             const float2 *cs) {
+  constexpr int N = 4;
   float a[N], b[N];
-  Chunk<T>::widen(*reinterpret_cast<const uint4 *>(src + c * N), a);
-  Chunk<T>::widen(*reinterpret_cast<const uint4 *>(src + c * N + D / 2), b);
+  Chunk<float>::widen(*reinterpret_cast<const uint4 *>(src + c * N), a);
+  Chunk<float>::widen(*reinterpret_cast<const uint4 *>(src + c * N + D / 2), b);
 #pragma unroll
   for (int e = 0; e < N; ++e) {
     float x = a[e], y = b[e];
@@ -65,17 +64,13 @@ __device__ __forceinline__ void load_rotated(const T *src, float *dst, int c, co
       const float2 r = cs[c * N + e];
       x = a[e] * r.x - b[e] * r.y;
       y = b[e] * r.x + a[e] * r.y;
-      if (round) {  // a key, as the cache will hold it
-        x = to_float<T>(from_float<T>(x));
-        y = to_float<T>(from_float<T>(y));
-      }
     }
     dst[c * N + e] = x;
     dst[c * N + e + D / 2] = y;
   }
 }
 
-template <typename T, int D, int kRows>
+template <int D, int kRows>
 __global__ void __launch_bounds__(kThreads)
     tree_simt_kernel(const TreeSimtArgs a) {
   using Smem = SimtSmem<D, kRows>;
@@ -84,7 +79,7 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kRT = kRows / 16;       // rows of a thread
   constexpr int kCT = D / 64;           // groups of 4 output columns of a thread
   constexpr int kTPR = kThreads / kRows;  // threads of a row in the softmax
-  constexpr int N = Chunk<T>::N;
+  constexpr int N = 4;  // elements of a 16-byte chunk
   const DeviceView &v = a.v;
   const TreeView &tv = a.tv;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -102,8 +97,8 @@ __global__ void __launch_bounds__(kThreads)
     for (int e = tid; e < kRows * (D / 2 / N); e += kThreads) {
       const int r = e / (D / 2 / N), c = e % (D / 2 / N);
       const int64_t i = draft0 + min(row0 + r, n - 1);
-      load_rotated<T, D>((const T *)a.q + (i * v.H + pc.h) * D, sm.q[r], c,
-                         v.rope ? tv.cs + i * (D / 2) : nullptr, false);
+      load_rotated<D>(a.q + (i * v.H + pc.h) * D, sm.q[r], c,
+                         v.rope ? tv.cs + i * (D / 2) : nullptr);
     }
     for (int r = tid; r < kRows; r += kThreads) {
       const int64_t i = draft0 + min(row0 + r, n - 1);
@@ -129,13 +124,13 @@ __global__ void __launch_bounds__(kThreads)
         if (drafts) {
           const int64_t i = draft0 + k0 + r;
           const int64_t off = (i * v.H + pc.h) * D;
-          load_rotated<T, D>((const T *)a.kd + off, sm.k[r], c,
-                             v.rope ? tv.cs + i * (D / 2) : nullptr, true);
-          load_rotated<T, D>((const T *)a.vd + off, sm.v[r], c, nullptr, false);
+          load_rotated<D>(a.kd + off, sm.k[r], c,
+                             v.rope ? tv.cs + i * (D / 2) : nullptr);
+          load_rotated<D>(a.vd + off, sm.v[r], c, nullptr);
         } else {
           const int64_t off = (pc.row0 + k0 + r) * D;
-          load_rotated<T, D>((const T *)a.kc + off, sm.k[r], c, nullptr, false);
-          load_rotated<T, D>((const T *)a.vc + off, sm.v[r], c, nullptr, false);
+          load_rotated<D>(a.kc + off, sm.k[r], c, nullptr);
+          load_rotated<D>(a.vc + off, sm.v[r], c, nullptr);
         }
       }
       if (!drafts && tid < kKeys) sm.age[tid] = slot_age(ring, k0 + tid);
@@ -254,9 +249,9 @@ __global__ void __launch_bounds__(kThreads)
         const int e = tx * 4 + 64 * c;
         if (pc.count == 1) {
           const float sum = sm.alpha[ty + 16 * i];
-          T *dst = (T *)a.out + ((draft0 + r) * v.H + pc.h) * D + e;
+          float *dst = a.out + ((draft0 + r) * v.H + pc.h) * D + e;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) dst[x] = from_float<T>(acc[i][4 * c + x] / sum);
+          for (int x = 0; x < 4; ++x) dst[x] = acc[i][4 * c + x] / sum;
         } else {
           *reinterpret_cast<float4 *>(tv.part_o + ((int64_t)p * tv.T + r) * D + e) =
               make_float4(acc[i][4 * c], acc[i][4 * c + 1], acc[i][4 * c + 2], acc[i][4 * c + 3]);
@@ -266,27 +261,27 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename T, int D, int kRows>
+template <int D, int kRows>
 cudaError_t set_attr() {
-  return cudaFuncSetAttribute(tree_simt_kernel<T, D, kRows>,
+  return cudaFuncSetAttribute(tree_simt_kernel<D, kRows>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)sizeof(SimtSmem<D, kRows>));
 }
 
-template <typename T, int D, int kRows>
+template <int D, int kRows>
 cudaError_t launch_t(const TreeSimtArgs &a, cudaStream_t s) {
-  cudaError_t e = set_attr<T, D, kRows>();
+  cudaError_t e = set_attr<D, kRows>();
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + kRows - 1) / kRows));
-  tree_simt_kernel<T, D, kRows><<<grid, kThreads, sizeof(SimtSmem<D, kRows>), s>>>(a);
+  tree_simt_kernel<D, kRows><<<grid, kThreads, sizeof(SimtSmem<D, kRows>), s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int D, int kRows>
+template <int D, int kRows>
 int ctas_t() {
   int n = 0;
-  if (set_attr<T, D, kRows>() != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, tree_simt_kernel<T, D, kRows>, kThreads,
+  if (set_attr<D, kRows>() != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, tree_simt_kernel<D, kRows>, kThreads,
                                                     sizeof(SimtSmem<D, kRows>)) != cudaSuccess ||
       n < 1)
     return 1;
@@ -295,29 +290,19 @@ int ctas_t() {
 
 }  // namespace
 
-int tree_simt_ctas_per_sm(int dtype, int head_dim, int n_rows) {
+int tree_simt_ctas_per_sm(int head_dim, int n_rows) {
   const bool small = n_rows <= 16;
-  if (dtype == RSWA_BF16) {
-    if (head_dim == 128)
-      return small ? ctas_t<__nv_bfloat16, 128, 16>() : ctas_t<__nv_bfloat16, 128, 64>();
-    return small ? ctas_t<__nv_bfloat16, 64, 16>() : ctas_t<__nv_bfloat16, 64, 64>();
-  }
-  if (head_dim == 128) return small ? ctas_t<float, 128, 16>() : ctas_t<float, 128, 64>();
-  return small ? ctas_t<float, 64, 16>() : ctas_t<float, 64, 64>();
+  if (head_dim == 128) return small ? ctas_t<128, 16>() : ctas_t<128, 64>();
+  return small ? ctas_t<64, 16>() : ctas_t<64, 64>();
 }
 
-cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const void *q,
-                             const void *kd, const void *vd, const void *kc, const void *vc,
-                             void *out, cudaStream_t s) {
+cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const float *q,
+                             const float *kd, const float *vd, const float *kc, const float *vc,
+                             float *out, cudaStream_t s) {
   const TreeSimtArgs a{v, tv, q, kd, vd, kc, vc, out};
   const bool small = tv.T <= 16;
-  if (v.dtype == RSWA_BF16) {
-    if (v.D == 128)
-      return small ? launch_t<__nv_bfloat16, 128, 16>(a, s) : launch_t<__nv_bfloat16, 128, 64>(a, s);
-    return small ? launch_t<__nv_bfloat16, 64, 16>(a, s) : launch_t<__nv_bfloat16, 64, 64>(a, s);
-  }
-  if (v.D == 128) return small ? launch_t<float, 128, 16>(a, s) : launch_t<float, 128, 64>(a, s);
-  return small ? launch_t<float, 64, 16>(a, s) : launch_t<float, 64, 64>(a, s);
+  if (v.D == 128) return small ? launch_t<128, 16>(a, s) : launch_t<128, 64>(a, s);
+  return small ? launch_t<64, 16>(a, s) : launch_t<64, 64>(a, s);
 }
 
 }  // namespace rswa

@@ -106,6 +106,39 @@ def test_tree_over_many_tiles_and_pieces(dtype, d):
     c.check(c.run(), rows=(0, 3, 8, 23))
 
 
+@pytest.mark.parametrize("T", [7, 64, 128])
+def test_tree_at_serving_sizes(T):
+    """Every SM at work on long prompts, the caches in HBM, again and again: no wait runs out,
+    and every pass gives the same."""
+    rswa = _rswa()
+    B, H, d, P, L = 4, 10, 128, 16000, 6
+    st = rswa.State(B, L, H, d, 128, [P] * B, dtype=BF, n_generated=[1000] * B)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    for x in st.k_cache + st.v_cache:
+        x.normal_(generator=g)
+    q, k, v = (torch.randn(B, T, H, d, generator=g, device="cuda").to(BF) for _ in range(3))
+    tree = st.tree(T)
+    first = [None] * L
+    for _ in range(5):
+        tree.set()
+        for layer in range(L):
+            out = torch.empty_like(q)
+            tree.attention(layer, q, k, v, out)
+            if first[layer] is None:
+                first[layer] = out
+            assert torch.equal(first[layer], out)
+    assert st.check() == 0
+    # the first draft of a chain, over the prompt, all but one of the ring, and itself
+    for layer in (0, L - 1):
+        for b, h in ((0, 0), (B - 1, H - 1)):
+            keep = [s for s in range(P + 128) if s != P + 1000 % 128]
+            ks, vs = (torch.cat([st.cache_view(layer, w, b, h)[keep], x[b, :1, h]]).double()
+                      for w, x in (("k", k), ("v", v)))
+            o, mass = ref.attend(q[b, 0, h], ks, vs, d ** -0.5)
+            err = (first[layer][b, 0, h].double() - o).abs()
+            assert bool((err <= ref.tolerance(o, mass, BF)).all())
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
 def test_tree_with_more_rings_than_ctas(dtype, d):
     B = 90
@@ -152,6 +185,35 @@ def test_values_a_draft_does_not_see_never_reach_it(dtype, d, bad):
     assert not bool(torch.isfinite(out[0, shallow, :, 7]).any())
     others = [e for e in range(d) if e != 7]
     assert torch.equal(out[:, shallow][..., others], clean[:, shallow][..., others])
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_values_that_every_draft_sees_reach_it(dtype, d, bad):
+    """A non-finite value in the prompt: that element takes it on, the others keep theirs."""
+    c = Case(dtype, d, 2, 16, (700,), (5,), 9, seed=7)
+    clean = c.run()
+    for h in range(2):
+        c.st.cache_view(0, "v", 0, h)[130, 7] = bad
+    out = c.run()
+    assert torch.equal(out[..., 7], torch.full_like(out[..., 7], bad)) or \
+        (bad != bad and bool(out[..., 7].isnan().all()))
+    others = [e for e in range(d) if e != 7]
+    assert torch.equal(out[..., others], clean[..., others])
+
+
+def test_dropped_copies_end_with_a_timeout_status():
+    """With the kernel's cache copies dropped every wait runs out, and says so."""
+    rswa = _rswa()
+    c = Case(BF, 128, 1, 8, (200,), (3,), 40)
+    c.run()
+    q, k, v = c.q.cuda(), c.k.cuda(), c.v.cuda()
+    out = torch.empty_like(q)
+    rswa.rswa_debug_inject_fault(c.st.handle, rswa.RSWA_FAULT_DROP_DECODE_COPIES)
+    c.tree.attention(0, q, k, v, out)
+    assert c.st.check() == rswa.RSWA_ETIMEOUT
+    rswa.rswa_debug_inject_fault(c.st.handle, 0)
+    c.check(c.run())
 
 
 @pytest.mark.parametrize("dtype,d", KINDS)
