@@ -118,6 +118,7 @@ struct TreeView {
   int32_t *parent;           // [B][T] as given to rswa_tree_set
   int32_t *depth;            // [B][T]
   uint4 *above;              // [B][T] bit j: row i attends to draft j (an ancestor or itself)
+  uint4 *below;              // [B][T] bit i: row i attends to this draft
   int32_t *n;                // [B] drafted tokens in use (0: the sequence's tree was refused)
   int32_t *accepted;         // [B] tokens the last commit took, until rswa_tree_advance
   float2 *cs;                // [B][T][D/2] (cos, sin) at every draft's position (RoPE)

@@ -177,6 +177,20 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The same, telling every thread whether `x` holds in any of them.
+__device__ __forceinline__ bool bar_red_or(int id, int nthreads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
 // ------------------------------------------------------------ conversions
 // A 16-byte chunk of elements widened to fp32.
 template <typename T>

@@ -76,16 +76,21 @@ __global__ void __launch_bounds__(RSWA_TREE_MAX)
     cur = nx;
     __syncthreads();
   }
-  if (i >= T) return;
-  const int64_t row = (int64_t)b * T + i;
   const int d = depth[cur][i];
   if (i < n && d >= v.W) {
     // the window ends below the path's first nodes
     for (int j = 0; j < i; ++j)
       if (depth[cur][j] < d - v.W + 1) above[cur][i][j >> 5] &= ~(1u << (j & 31));
   }
+  __syncthreads();
+  if (i >= T) return;
+  uint32_t below[4] = {0u, 0u, 0u, 0u};
+  for (int j = i; j < n; ++j)  // a draft's row number is above its ancestors'
+    below[j >> 5] |= ((above[cur][j][i >> 5] >> (i & 31)) & 1u) << (j & 31);
+  const int64_t row = (int64_t)b * T + i;
   tv.parent[row] = pr;
   tv.depth[row] = d;
+  tv.below[row] = make_uint4(below[0], below[1], below[2], below[3]);
   tv.above[row] = make_uint4(above[cur][i][0], above[cur][i][1], above[cur][i][2], above[cur][i][3]);
 }
 
@@ -276,8 +281,8 @@ DecodePlan plan_for(const rswa_state *s, int T) {
 }
 
 struct TreeLayout {
-  size_t pieces, cta_piece, bh_piece, uploaded, n, accepted, parent, depth, above, cs, part_ml,
-      part_o, total;
+  size_t pieces, cta_piece, bh_piece, uploaded, n, accepted, parent, depth, above, below, cs,
+      part_ml, part_o, total;
 };
 
 TreeLayout layout_tree(const rswa_state *s, int T, const DecodePlan &p) {
@@ -299,6 +304,7 @@ TreeLayout layout_tree(const rswa_state *s, int T, const DecodePlan &p) {
   w.parent = take(rows * sizeof(int32_t));
   w.depth = take(rows * sizeof(int32_t));
   w.above = take(rows * sizeof(uint4));
+  w.below = take(rows * sizeof(uint4));
   w.cs = take(rows * (d / 2) * sizeof(float2));
   w.part_ml = take((size_t)p.n_pieces * (size_t)T * sizeof(float2));
   w.part_o = take((size_t)p.n_pieces * (size_t)T * d * sizeof(float));
@@ -396,6 +402,7 @@ rswa_status rswa_tree_create(rswa_state *state, int32_t max_draft, void *workspa
     tv.parent = (int32_t *)(base + w.parent);
     tv.depth = (int32_t *)(base + w.depth);
     tv.above = (uint4 *)(base + w.above);
+    tv.below = (uint4 *)(base + w.below);
     tv.n = (int32_t *)(base + w.n);
     tv.accepted = (int32_t *)(base + w.accepted);
     tv.cs = (float2 *)(base + w.cs);
