@@ -223,6 +223,25 @@ int decode_ctas_per_sm(int dtype, int head_dim);
 // Clusters of `cluster` decode CTAs that can be resident at once (0: none).
 int decode_max_clusters(int dtype, int head_dim, int cluster);
 
+// A launch that may begin while the kernel before it in the stream still runs:
+// the kernel calls grid_dependency_wait() before it touches what that one reads
+// or writes, and allow_dependents() only after that.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t s, const A &...args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = block;
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, args...);
+}
+
 // Host-side helpers of the planner (rswa_api.cu).
 bool config_ok(const rswa_config *c, const int64_t *plen);
 int current_device();

@@ -44,6 +44,8 @@ __global__ void __launch_bounds__(RSWA_TREE_MAX)
   __shared__ int depth[2][RSWA_TREE_MAX], up[2][RSWA_TREE_MAX];
   const int b = blockIdx.x, i = threadIdx.x;
   const int T = tv.T;
+  grid_dependency_wait();
+  allow_dependents();
   int n = n_draft ? n_draft[b] : T;
   const bool bad_len = n < 0 || n > T;
   if (bad_len) n = 0;
@@ -96,44 +98,76 @@ __global__ void __launch_bounds__(RSWA_TREE_MAX)
 
 // ------------------------------------------------------- merge of partials
 // out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p over the pieces p of a
-// ring, M = max_p m_p.  One CTA per ring and group of rows; a thread holds 4
-// neighbouring elements of one row.
-constexpr int kMergeThreads = 256;
+// ring, M = max_p m_p.  One warp per ring and row: lane p holds the (m, l) of
+// piece p (32 at a time), then every lane D / 32 elements of the output, with
+// eight pieces' loads in flight.  Latency-bound.
+constexpr int kMergeWarps = 4;
+constexpr int kMergeAhead = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(kMergeWarps * 32)
     tree_combine_kernel(const DeviceView v, const TreeView tv, T *out) {
-  constexpr int kPerRow = D / 4;
-  constexpr int kRows = kMergeThreads / kPerRow;
-  const int groups = (tv.T + kRows - 1) / kRows;
-  const int bh = (int)(blockIdx.x / (unsigned)groups);
-  const int p0 = tv.bh_piece[bh], p1 = tv.bh_piece[bh + 1];
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t id = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int64_t bh = id / tv.T;
+  const int i = (int)(id % tv.T);
+  const bool any = bh < (int64_t)v.B * v.H;
+  const int p0 = any ? tv.bh_piece[bh] : 0, p1 = any ? tv.bh_piece[bh + 1] : 0;
+  grid_dependency_wait();
+  allow_dependents();
   if (p1 - p0 < 2) return;  // its one piece wrote the output
-  const int b = bh / v.H, h = bh % v.H;
-  const int i = (int)(blockIdx.x % (unsigned)groups) * kRows + (int)threadIdx.x / kPerRow;
-  const int e = (int)(threadIdx.x % kPerRow) * 4;
+  const int b = (int)(bh / v.H), h = (int)(bh % v.H);
   if (i >= tv.n[b]) return;
-  float m = -INFINITY;
-  for (int p = p0; p < p1; ++p) m = fmaxf(m, tv.part_ml[(int64_t)p * tv.T + i].x);
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = p0; p < p1; ++p) {
-    const float2 ml = tv.part_ml[(int64_t)p * tv.T + i];
-    if (ml.x == -INFINITY && !(ml.y > 0.f) && !(ml.y != ml.y)) continue;  // nothing seen there
-    const float4 o = *reinterpret_cast<const float4 *>(tv.part_o + ((int64_t)p * tv.T + i) * D + e);
-    const float w = ml.x == m ? 1.f : exp2f(ml.x - m);
-    l = fmaf(w, ml.y, l);
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
+  float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int c0 = p0; c0 < p1; c0 += 32) {
+    const int cnt = min(32, p1 - c0);
+    const float2 ml = lane < cnt ? tv.part_ml[(int64_t)(c0 + lane) * tv.T + i]
+                                 : make_float2(-INFINITY, 0.f);
+    // a piece in which the row saw nothing has no o; one of NaN scores has l = NaN
+    const bool seen = ml.x != -INFINITY || ml.y != 0.f;
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float m_new = fmaxf(m, top);
+    const float w = !seen ? 0.f : ml.x == m_new ? 1.f : exp2f(ml.x - m_new);
+    float lc = seen ? w * ml.y : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lc += __shfl_xor_sync(0xffffffffu, lc, o);
+    const float corr = m == m_new ? 1.f : exp2f(m - m_new);
+    l = fmaf(l, corr, lc);
+    m = m_new;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= corr;
+    const uint32_t use = __ballot_sync(0xffffffffu, seen);
+    for (int j0 = 0; j0 < cnt; j0 += kMergeAhead) {
+      float o[kMergeAhead][E];
+#pragma unroll
+      for (int u = 0; u < kMergeAhead; ++u) {
+        const float *src = tv.part_o + ((int64_t)(c0 + j0 + u) * tv.T + i) * D + lane * E;
+        if (j0 + u < 32 && ((use >> ((j0 + u) & 31)) & 1u)) {
+          if constexpr (E == 4)
+            *reinterpret_cast<float4 *>(o[u]) = *reinterpret_cast<const float4 *>(src);
+          else
+            *reinterpret_cast<float2 *>(o[u]) = *reinterpret_cast<const float2 *>(src);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kMergeAhead; ++u) {
+        const float wj = __shfl_sync(0xffffffffu, w, (j0 + u) & 31);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wj, o[u][e], acc[e]);
+      }
+    }
   }
-  T *dst = out + (((int64_t)b * tv.T + i) * v.H + h) * D + e;
-  dst[0] = from_float<T>(acc.x / l);
-  dst[1] = from_float<T>(acc.y / l);
-  dst[2] = from_float<T>(acc.z / l);
-  dst[3] = from_float<T>(acc.w / l);
+  T *dst = out + (((int64_t)b * tv.T + i) * v.H + h) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) dst[e] = from_float<T>(acc[e] / l);
 }
 
 // ------------------------------------------------------------------ commit
@@ -321,17 +355,17 @@ bool tree_args_ok(const rswa_state *s, int32_t max_draft) {
 
 cudaError_t launch_tree_set(const DeviceView &v, const TreeView &tv, const int32_t *parent,
                             const int32_t *n_draft, cudaStream_t s) {
-  tree_set_kernel<<<v.B, RSWA_TREE_MAX, 0, s>>>(v, tv, parent, n_draft);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_overlapped(tree_set_kernel, dim3((unsigned)v.B), dim3(RSWA_TREE_MAX), 0, s,
+                                    v, tv, parent, n_draft);
   return e != cudaSuccess ? e : launch_tree_rope(v, tv, s);
 }
 
 template <typename T, int D>
 static cudaError_t combine_t(const DeviceView &v, const TreeView &tv, void *out, cudaStream_t s) {
-  constexpr int kRows = kMergeThreads / (D / 4);
-  const unsigned groups = (unsigned)((tv.T + kRows - 1) / kRows);
-  tree_combine_kernel<T, D><<<(unsigned)(v.B * v.H) * groups, kMergeThreads, 0, s>>>(v, tv, (T *)out);
-  return cudaGetLastError();
+  const int64_t rows = (int64_t)v.B * v.H * tv.T;
+  return launch_overlapped(tree_combine_kernel<T, D>,
+                           dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
+                           dim3(kMergeWarps * 32), 0, s, v, tv, (T *)out);
 }
 
 cudaError_t launch_tree_combine(const DeviceView &v, const TreeView &tv, void *out,

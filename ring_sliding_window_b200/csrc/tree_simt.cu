@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(kThreads)
   const int row0 = (int)blockIdx.y * kRows;
   const int n_draft_tiles = (tv.T + kKeys - 1) / kKeys;
   const float qs = v.scale * kLog2e;
+  grid_dependency_wait();
+  allow_dependents();
 
   for (int p = tv.cta_piece[blockIdx.x]; p < tv.cta_piece[blockIdx.x + 1]; ++p) {
     const DecodePiece pc = tv.pieces[p];
@@ -273,8 +275,8 @@ cudaError_t launch_t(const TreeSimtArgs &a, cudaStream_t s) {
   cudaError_t e = set_attr<D, kRows>();
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + kRows - 1) / kRows));
-  tree_simt_kernel<D, kRows><<<grid, kThreads, sizeof(SimtSmem<D, kRows>), s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(tree_simt_kernel<D, kRows>, grid, dim3(kThreads),
+                           sizeof(SimtSmem<D, kRows>), s, a);
 }
 
 template <int D, int kRows>

@@ -56,6 +56,7 @@ constexpr int kTile = kTreeTcTile;          // keys per tile
 constexpr int kHalfBytes = kTile * 64 * 2;  // one 64-column swizzled block: 16 KB
 constexpr float kGrowth = 8.0f;             // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kScan = 4;  // chunks of a row of V looked at together
 
 template <int D, int N>
 struct Shape {
@@ -184,7 +185,16 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_addr, uint3
                accumulate || kk > 0);
 }
 
-__device__ __forceinline__ bool finite_bf16(uint32_t x) { return (x & 0x7f80u) != 0x7f80u; }
+// Bit 15 / 31: the low / high bf16 of a pair is not finite (its exponent's ones
+// carry over).
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+// A pair with 0 where it is not finite.
+__device__ __forceinline__ uint32_t finite_part(uint32_t x) {
+  const uint32_t t = not_finite(x);
+  return x & ~((t & 0x8000u ? 0xffffu : 0u) | (t & 0x80000000u ? 0xffff0000u : 0u));
+}
 
 // NC (16 or 32) consecutive TMEM columns of this thread's lane.
 template <int NC>
@@ -268,6 +278,21 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     sm.dead = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x < 4) sm.bad[threadIdx.x] = 0u;
+  if (warp == kProducer && lane == 0) {
+    // the plan and the maps are the tree's own; the first tiles' way to L2 can
+    // begin while the kernel before this one still runs (a hint returns nothing)
+    const DecodePiece pc = tv.pieces[p_begin];
+    tc::prefetch_tmap(&tm_q);
+    tc::prefetch_tmap(&tm_kc);
+    tc::prefetch_tmap(&tm_vc);
+    const int first = max(0, pc.key_begin - 1);
+    for (int t = first; t < min(pc.key_end - 1, first + NST); ++t)
+      for (int x = 0; x < kHalves; ++x) {
+        tc::tma_prefetch_2d(&tm_kc, 64 * x, (int)(pc.row0 + (int64_t)t * kTile));
+        tc::tma_prefetch_2d(&tm_vc, 64 * x, (int)(pc.row0 + (int64_t)t * kTile));
+      }
+  }
   if (warp == kMma) {
     tc::tmem_alloc(&sm.tmem_base, S::kTmemCols);
     tc::tmem_relinquish();
@@ -277,15 +302,14 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tbase = sm.tmem_base;
   volatile int *dead = &sm.dead;
+  grid_dependency_wait();
+  allow_dependents();
 
   if (warp == kProducer) {
     // -------------------------------------------------------------- producer
     // test-only fault injection: no loads at all, so every wait runs out
     const bool drop = (*v.fault & RSWA_FAULT_DROP_DECODE_COPIES) != 0;
     if (lane == 0 && !drop) {
-      tc::prefetch_tmap(&tm_q);
-      tc::prefetch_tmap(&tm_kc);
-      tc::prefetch_tmap(&tm_vc);
       constexpr uint32_t kDraftBytes = (uint32_t)N * 128u * kHalves;
       int it = 0, active = 0;
       bool ok = true;
@@ -537,36 +561,32 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           // V's rows that hold no entry become 0, and so do values that are not finite
           const int held = drafts ? n : ring.held - k0;
           bool bad = false;
-          if (group == 0) {
-            wait(&sm.v_full[it % NST], (it / NST) & 1);
-            uint8_t *vt = sm.v[it % NST];
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              uint4 *at = reinterpret_cast<uint4 *>(vt + chunk_at(key, c, kHalfBytes));
-              if (key >= held) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-              }
-              const uint4 u = *at;
-              uint32_t w[4] = {u.x, u.y, u.z, u.w};
-              bool touched = false;
+          wait(&sm.v_full[it % NST], (it / NST) & 1);
+          uint8_t *vt = sm.v[it % NST];
+          constexpr int kMine = D / 8 / S::kGroups;  // this group's chunks of the row
+          for (int c0 = group * kMine; c0 < (group + 1) * kMine; c0 += kScan) {
+            uint4 u[kScan];
+            uint32_t t = 0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const bool f0 = finite_bf16(w[e]), f1 = finite_bf16(w[e] >> 16);
-                if (!f0) w[e] &= 0xffff0000u;
-                if (!f1) w[e] &= 0x0000ffffu;
-                touched |= !f0 || !f1;
-              }
-              if (touched) {
-                *at = make_uint4(w[0], w[1], w[2], w[3]);
-                bad = true;
-              }
-            }
+            for (int c = 0; c < kScan; ++c)
+              u[c] = *reinterpret_cast<const uint4 *>(vt + chunk_at(key, c0 + c, kHalfBytes));
+#pragma unroll
+            for (int c = 0; c < kScan; ++c)
+              t |= not_finite(u[c].x) | not_finite(u[c].y) | not_finite(u[c].z) | not_finite(u[c].w);
+            if (key < held && !t) continue;
+            bad |= key < held;
+#pragma unroll
+            for (int c = 0; c < kScan; ++c)
+              *reinterpret_cast<uint4 *>(vt + chunk_at(key, c0 + c, kHalfBytes)) =
+                  key < held ? make_uint4(finite_part(u[c].x), finite_part(u[c].y),
+                                          finite_part(u[c].z), finite_part(u[c].w))
+                             : make_uint4(0u, 0u, 0u, 0u);
           }
+          __syncwarp();
           mend = bar_red_or(5, kAll, bad);
           if (mend) {
             const uint32_t word = __ballot_sync(0xffffffffu, bad);
-            if (group == 0 && lane == 0) sm.bad[warp] = word;
+            if (lane == 0) atomicOr(&sm.bad[warp & 3], word);
           }
         }
         fence_proxy_async_smem();
@@ -607,6 +627,8 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           }
           tc::fence_before_sync();
           named_bar_sync(5, kAll);  // sm.bad is read
+          if (threadIdx.x < 4) sm.bad[threadIdx.x] = 0u;
+          __syncwarp();
         }
       }
       // the piece's result: final where it is the ring's only one, else a partial
@@ -636,19 +658,22 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         __syncwarp();
         named_bar_sync(bar_group, 128);
       }
-      float o[NC], o_lo[NC];
-      load_cols<NC>(t_hi, o);
-      load_cols<NC>(t_lo, o_lo);
+#pragma unroll 1
+      for (int c0 = 0; c0 < NC && col0 + c0 < n; c0 += 8) {
+        float o[8], o_lo[8];
+        tc::ld8(t_hi + (uint32_t)c0, reinterpret_cast<uint32_t *>(o));
+        tc::ld8(t_lo + (uint32_t)c0, reinterpret_cast<uint32_t *>(o_lo));
+        tc::wait_ld();
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int i = col0 + c;
-        if (i >= n) break;
-        const float x = isfinite(o[c]) ? o[c] + o_lo[c] : o[c];
-        if (!has_elem) continue;
-        if (pc.count == 1)
-          a.out[((draft0 + i) * v.H + pc.h) * D + elem] = __float2bfloat16_rn(x / sm.alpha[i]);
-        else
-          tv.part_o[((int64_t)p * tv.T + i) * D + elem] = x;
+        for (int c = 0; c < 8; ++c) {
+          const int i = col0 + c0 + c;
+          const float x = isfinite(o[c]) ? o[c] + o_lo[c] : o[c];
+          if (i >= n || !has_elem) continue;
+          if (pc.count == 1)
+            a.out[((draft0 + i) * v.H + pc.h) * D + elem] = __float2bfloat16_rn(x / sm.alpha[i]);
+          else
+            tv.part_o[((int64_t)p * tv.T + i) * D + elem] = x;
+        }
       }
     }
   }
@@ -680,8 +705,8 @@ cudaError_t launch_t(const DeviceView &v, const TreeView &tv, const CUtensorMap 
     return cudaErrorInvalidValue;
   const TreeTcArgs args{v, tv, (const __nv_bfloat16 *)vd, (const __nv_bfloat16 *)vc,
                         (__nv_bfloat16 *)out};
-  tree_tc_kernel<D, N><<<tv.grid, Shape<D, N>::kThreads, smem, s>>>(tq, tk, tvv, tkc, tvc, args);
-  return cudaGetLastError();
+  return launch_overlapped(tree_tc_kernel<D, N>, dim3((unsigned)tv.grid),
+                           dim3(Shape<D, N>::kThreads), (size_t)smem, s, tq, tk, tvv, tkc, tvc, args);
 }
 
 template <int D>

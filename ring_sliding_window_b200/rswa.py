@@ -158,20 +158,15 @@ def _check(status: int, what: str) -> None:
         raise RswaError(status, what)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    if t is None:
-        return ctypes.c_void_p(0)
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    return ctypes.c_void_p(t.data_ptr())
+def _ptr(t):
+    """The address that a c_void_p argument takes (None: NULL)."""
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _i64(vals: Sequence[int]):
@@ -194,8 +189,8 @@ def rswa_workspace_bytes(cfg: rswa_config, prefill_len: Sequence[int]) -> int:
 
 def rswa_state_create(cfg, prefill_len, n_generated, k_cache, v_cache, workspace,
                       workspace_size, stream=None) -> ctypes.c_void_p:
-    kp = (ctypes.c_void_p * len(k_cache))(*[_ptr(t).value for t in k_cache])
-    vp = (ctypes.c_void_p * len(v_cache))(*[_ptr(t).value for t in v_cache])
+    kp = (ctypes.c_void_p * len(k_cache))(*[_ptr(t) for t in k_cache])
+    vp = (ctypes.c_void_p * len(v_cache))(*[_ptr(t) for t in v_cache])
     out = ctypes.c_void_p()
     st = lib.rswa_state_create(ctypes.byref(cfg), _i64(prefill_len),
                                None if n_generated is None else _i64(n_generated), kp, vp,
@@ -207,8 +202,8 @@ def rswa_state_create(cfg, prefill_len, n_generated, k_cache, v_cache, workspace
 
 def rswa_state_create_pooled(cfg, prefill_len, n_generated, slot_base, pool_slots, k_cache,
                              v_cache, workspace, workspace_size, stream=None) -> ctypes.c_void_p:
-    kp = (ctypes.c_void_p * len(k_cache))(*[_ptr(t).value for t in k_cache])
-    vp = (ctypes.c_void_p * len(v_cache))(*[_ptr(t).value for t in v_cache])
+    kp = (ctypes.c_void_p * len(k_cache))(*[_ptr(t) for t in k_cache])
+    vp = (ctypes.c_void_p * len(v_cache))(*[_ptr(t) for t in v_cache])
     out = ctypes.c_void_p()
     st = lib.rswa_state_create_pooled(ctypes.byref(cfg), _i64(prefill_len),
                                       None if n_generated is None else _i64(n_generated),
@@ -383,8 +378,8 @@ def rswa_tree_attention(tree, layer, q, k_draft, v_draft, out, stream=None) -> N
 
 def rswa_tree_commit(tree, k_draft, v_draft, path, path_len, stream=None) -> None:
     """k_draft, v_draft: one tensor a layer; path: cuda int32 [B, T]; path_len: cuda int32 [B]."""
-    kp = (ctypes.c_void_p * len(k_draft))(*[_ptr(t).value for t in k_draft])
-    vp = (ctypes.c_void_p * len(v_draft))(*[_ptr(t).value for t in v_draft])
+    kp = (ctypes.c_void_p * len(k_draft))(*[_ptr(t) for t in k_draft])
+    vp = (ctypes.c_void_p * len(v_draft))(*[_ptr(t) for t in v_draft])
     _check(lib.rswa_tree_commit(tree, kp, vp, _ptr(path), _ptr(path_len), _stream(stream)),
            "rswa_tree_commit")
 
@@ -458,13 +453,13 @@ def rswa_debug_inject_fault(state, flags: int, stream=None) -> None:
 
 
 # --------------------------------------------------------- argument checks
-def _require(t, what: str, shape, dtype, device) -> None:
+def _require(t, what: str, shape: tuple, dtype, device) -> None:
     """The C calls take bare pointers: a tensor of another type, shape, layout or
     device would be read as if it had these."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or \
             not t.is_contiguous() or t.device != device:
         raise RswaError(RSWA_EINVAL, f"{what}: needs a contiguous {dtype} tensor "
-                                     f"{tuple(shape)} on {device}")
+                                     f"{shape} on {device}")
 
 
 # ---------------------------------------------------------- owning helper
@@ -548,7 +543,6 @@ class State:
                             stream=None):
         rswa_decode_step_partial(self.handle, layer, q, k_new, v_new, key_lo, key_hi, part_ml,
                                  part_o, stream)
-
 
     def tree(self, max_draft: int, stream=None) -> "Tree":
         """Trees of up to max_draft drafted tokens a sequence over this state."""
