@@ -56,7 +56,6 @@ constexpr int kTile = kTreeTcTile;          // keys per tile
 constexpr int kHalfBytes = kTile * 64 * 2;  // one 64-column swizzled block: 16 KB
 constexpr float kGrowth = 8.0f;             // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kScan = 4;  // chunks of a row of V looked at together
 
 template <int D, int N>
 struct Shape {
@@ -85,7 +84,7 @@ struct __align__(1024) TreeSmem {
   float neg_m[N];   // -m of every draft
   float alpha[N];   // factors of a growth; at a piece's end the sums
   int top[N];       // largest scores of a tile, as ordered_int (INT_MIN between growths)
-  uint8_t depth[N];
+  __align__(4) uint8_t depth[N];
   uint64_t q_full, q_free;
   uint64_t k_full[S::kStages], k_empty[S::kStages];
   uint64_t v_full[S::kStages], v_empty[S::kStages];
@@ -440,11 +439,13 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.turned);
       }
       ++active;
-      // m starts below every score; a column that holds no draft never grows
-      if (tid < N) {
-        sm.neg_m[tid] = tid < n ? FLT_MAX : -FLT_MAX;
-        sm.top[tid] = INT_MIN;
-        sm.depth[tid] = (uint8_t)(tid < n ? tv.depth[draft0 + tid] : 0);
+      // m starts below every score; a column that holds no draft never grows.  (Each
+      // group's own columns: another may still be at the previous piece's end.)
+      if (key < NC) {
+        const int c = col0 + key;
+        sm.neg_m[c] = c < n ? FLT_MAX : -FLT_MAX;
+        sm.top[c] = INT_MIN;
+        sm.depth[c] = (uint8_t)(c < n ? tv.depth[draft0 + c] : 0);
       }
       __syncwarp();
       named_bar_sync(5, kAll);
@@ -465,17 +466,28 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           } else {
             const int age = slot_age(ring, k0 + key);
             const int deepest = age == INT_MIN ? INT_MAX : age == INT_MAX ? -1 : v.W - 1 - age;
-            sees = 0;
-#pragma unroll 8
-            for (int c = 0; c < NC; ++c)
-              sees |= (sm.depth[col0 + c] <= deepest ? 1u : 0u) << c;
+            if (deepest >= RSWA_TREE_MAX || deepest < 0) {
+              sees = deepest < 0 ? 0u : 0xffffffffu;
+            } else {
+              // four depths at a time: a byte of ones where the draft sees the key,
+              // of which byte i gives bit i
+              sees = 0;
+#pragma unroll
+              for (int c = 0; c < NC; c += 4) {
+                const uint32_t d4 = *reinterpret_cast<const uint32_t *>(&sm.depth[col0 + c]);
+                const uint32_t le = __vcmpleu4(d4, (uint32_t)deepest * 0x01010101u);
+                sees |= (((le & 0x08040201u) * 0x01010101u) >> 24) << c;
+              }
+            }
           }
         }
         wait(&sm.s_full[it & 1], (it >> 1) & 1);
         tc::fence_after_sync();
         float x[NC];
+        // pass 0: the scores less m; where one exceeds it by more than kGrowth (as
+        // in every first tile), pass 2 moves m and pass 3 is pass 0 again
 #pragma unroll 1
-        for (int pass = 0;; ++pass) {
+        for (int pass = j == 0 ? 2 : 0;; ++pass) {
           load_cols<NC>(t_s, x);
           if (masked) {
 #pragma unroll
@@ -529,7 +541,6 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
             x[c + 3] = tc::f2_hi(a1);
             top = tc::fmax3(tc::fmax3(top, x[c], x[c + 1]), x[c + 2], x[c + 3]);
           }
-          // pass 0 may ask for pass 2 (growth), which pass 3 follows
           if (pass == 3 || !bar_red_or(bar_group, 128, top > kGrowth)) break;
           pass = 1;
         }
@@ -564,6 +575,8 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           wait(&sm.v_full[it % NST], (it / NST) & 1);
           uint8_t *vt = sm.v[it % NST];
           constexpr int kMine = D / 8 / S::kGroups;  // this group's chunks of the row
+          constexpr int kScan = kMine < 8 ? kMine : 8;  // loaded together
+          static_assert(kMine % kScan == 0, "whole batches");
           for (int c0 = group * kMine; c0 < (group + 1) * kMine; c0 += kScan) {
             uint4 u[kScan];
             uint32_t t = 0;
@@ -648,7 +661,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         named_bar_sync(bar_group, 128);
         if (key < NC) {
           const float l = (red[key] + red[NC + key]) + (red[2 * NC + key] + red[3 * NC + key]);
-          sm.alpha[col0 + key] = l;
+          sm.alpha[col0 + key] = 1.f / l;
           if (pc.count > 1 && col0 + key < n) {
             const float m = -sm.neg_m[col0 + key];
             tv.part_ml[(int64_t)p * tv.T + col0 + key] =
@@ -658,22 +671,31 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         __syncwarp();
         named_bar_sync(bar_group, 128);
       }
+      const bool whole = pc.count == 1;
+      __nv_bfloat16 *dst = a.out + ((draft0 + col0) * v.H + pc.h) * D + elem;
+      float *part = tv.part_o + ((int64_t)p * tv.T + col0) * D + elem;
+      const int row_step = v.H * D;
 #pragma unroll 1
       for (int c0 = 0; c0 < NC && col0 + c0 < n; c0 += 8) {
         float o[8], o_lo[8];
         tc::ld8(t_hi + (uint32_t)c0, reinterpret_cast<uint32_t *>(o));
         tc::ld8(t_lo + (uint32_t)c0, reinterpret_cast<uint32_t *>(o_lo));
         tc::wait_ld();
+        if (has_elem) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int i = col0 + c0 + c;
-          const float x = isfinite(o[c]) ? o[c] + o_lo[c] : o[c];
-          if (i >= n || !has_elem) continue;
-          if (pc.count == 1)
-            a.out[((draft0 + i) * v.H + pc.h) * D + elem] = __float2bfloat16_rn(x / sm.alpha[i]);
-          else
-            tv.part_o[((int64_t)p * tv.T + i) * D + elem] = x;
+          for (int c = 0; c < 8; ++c) {
+            if (isfinite(o[c])) o[c] += o_lo[c];
+            if (col0 + c0 + c < n) {
+              if (whole)
+                dst[c * row_step] = __float2bfloat16_rn(o[c] * sm.alpha[col0 + c0 + c]);
+              else
+                part[c * D] = o[c];
+            }
+          }
         }
+        __syncwarp();
+        dst += 8 * row_step;
+        part += 8 * D;
       }
     }
   }

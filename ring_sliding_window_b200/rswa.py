@@ -159,8 +159,8 @@ def _check(status: int, what: str) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream() without its stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -477,6 +477,7 @@ class State:
         if wb == 0:
             raise RswaError(RSWA_EINVAL, "rswa_workspace_bytes")
         self.workspace = torch.empty(wb, dtype=torch.uint8, device=device)
+        self._device = self.workspace.device
         if pool is not None:
             # requests placed in a TokenPool's caches at the given slot bases
             self.k_cache, self.v_cache = pool.k_cache, pool.v_cache
@@ -548,10 +549,6 @@ class State:
         """Trees of up to max_draft drafted tokens a sequence over this state."""
         return Tree(self, max_draft, stream)
 
-    @property
-    def _device(self):
-        return self.workspace.device
-
     def score_buffer(self) -> torch.Tensor:
         """A layer's accumulated attention weights, all zero."""
         return torch.zeros(rswa_score_bytes(self.handle) // 4, dtype=torch.float32,
@@ -595,6 +592,7 @@ class Tree:
 
     def __init__(self, state: State, max_draft: int, stream=None):
         self.state, self.T = state, int(max_draft)
+        self._shape = (state.B, self.T, state.H, state.d)
         wb = rswa_tree_workspace_bytes(state.handle, self.T)
         if wb == 0:
             raise RswaError(RSWA_EINVAL, "rswa_tree_workspace_bytes")
@@ -602,8 +600,7 @@ class Tree:
         self.handle = rswa_tree_create(state.handle, self.T, self.workspace, wb, stream)
 
     def _drafts(self, t, what):
-        st = self.state
-        _require(t, what, (st.B, self.T, st.H, st.d), st.dtype, st._device)
+        _require(t, what, self._shape, self.state.dtype, self.state._device)
 
     def set(self, parent=None, n_draft=None, stream=None):
         st = self.state
@@ -614,8 +611,10 @@ class Tree:
         rswa_tree_set(self.handle, parent, n_draft, stream)
 
     def attention(self, layer, q, k_draft, v_draft, out, stream=None):
-        for t, what in ((q, "q"), (k_draft, "k_draft"), (v_draft, "v_draft"), (out, "out")):
-            self._drafts(t, what)
+        self._drafts(q, "q")
+        self._drafts(k_draft, "k_draft")
+        self._drafts(v_draft, "v_draft")
+        self._drafts(out, "out")
         rswa_tree_attention(self.handle, layer, q, k_draft, v_draft, out, stream)
 
     def commit(self, k_draft, v_draft, path, path_len, stream=None):
