@@ -310,7 +310,11 @@ DecodePlan plan_tree(const rswa_state *s, int T, int tile, int ctas) {
 }
 
 DecodePlan plan_for(const rswa_state *s, int T) {
-  if (s->cfg.dtype == RSWA_BF16) return plan_tree(s, T, kTreeTcTile, s->num_sms);
+  if (s->cfg.dtype == RSWA_BF16) {
+    // the tensor-core kernel: one CTA an SM for every kTreeTcRows drafts
+    const int cols = (T + kTreeTcRows - 1) / kTreeTcRows;
+    return plan_tree(s, T, kTreeTcTile, std::max(1, s->num_sms / cols));
+  }
   return plan_tree(s, T, kTreeSimtTile, s->num_sms * tree_simt_ctas_per_sm(s->cfg.head_dim, T));
 }
 

@@ -17,12 +17,20 @@
 //   MMA warp        one thread: S^T = K Q^T (128 keys x N drafts) into one of
 //                   two TMEM buffers, a tile ahead of O^T += V^T P;
 //   softmax warps   thread r of four warps owns key r of the tile (TMEM lane r)
-//                   and up to 32 drafts: 4, 8 or 16 warps.
+//                   and up to 32 drafts: 4 warps, or 8 for N = 64;
+//   4 side warps    what would hold the softmax up where pieces begin and end:
+//                   the scan of V (below), RoPE, and the results of a piece,
+//                   while the next one already fills the other O.
 // With the keys on the lanes the work of a tile grows with the drafts (N = 16,
-// 32, 64 or 128), and all lanes take part however few they are.  What a softmax
-// needs across the lanes is kept off the ordinary tile: the subtracted m_i only
-// moves when a score exceeds it by more than 2^8, which one barrier with an OR
-// finds out, and the sums over the keys stay per lane until a piece ends.
+// 32 or 64), and all lanes take part however few they are.  What a softmax needs
+// across the lanes is kept off the ordinary tile: the subtracted m_i only moves
+// when a score exceeds it by more than 2^8, which one barrier with an OR finds
+// out, and the sums over the keys stay per lane until a piece ends.
+//
+// More than 64 drafts are two columns of the grid with N = 64: half the SMs
+// each, over the same tiles at the same time, so HBM is read about once.  (One
+// CTA with N = 128 has no registers and shared memory left to keep the tensor
+// cores busy: 140 us against TODO for 128 drafts over 4 x 16,384 tokens.)
 //
 // P goes to the MMA as a bf16 pair hi + lo, next to one another along N, so one
 // product gives O_hi | O_lo (relative error of a weight 2^-15; bf16 alone would
@@ -32,11 +40,11 @@
 //
 // A masked score becomes -inf, so its weight is 0, but 0 x inf is NaN inside
 // an MMA.  In the tiles that hold masked entries (the drafts, and the tiles
-// with ring slots) the softmax threads therefore take non-finite values out of
-// V's shared-memory copy, and add them to the drafts that do see them, by hand.
+// with ring slots) the side warps therefore take non-finite values out of V's
+// shared-memory copy, and add them to the results of the drafts that see them.
 //
 // A wait that runs out leaves the softmax warps going through all their tiles
-// without waiting (their barriers need every warp); the other two stop.
+// without waiting (their barriers need every warp), and the side warps; the others stop.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -60,9 +68,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 template <int D, int N>
 struct Shape {
   static constexpr int kGroups = N <= 32 ? 1 : N / 32;  // of 4 softmax warps
-  static constexpr int NC = N / kGroups;             // drafts of a softmax thread
+  static constexpr int NC = N / kGroups;                // drafts of a softmax thread
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kThreads = (kSoftWarps + 2) * 32;
+  static constexpr int kThreads = (kSoftWarps + 6) * 32;
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kHalfBytes;
   static constexpr int kPBytes = N <= 32 ? kHalfBytes : N / 32 * kHalfBytes;
@@ -70,7 +78,8 @@ struct Shape {
   // larger P; P twice where it fits
   static constexpr int kStages = (N <= 32 ? 3 : 2) * (D == 64 ? 2 : 1);
   static constexpr int kPBufs = N == 64 ? 2 : 1;
-  static constexpr uint32_t kTmemCols = 4 * N;       // S0, S1, O_hi, O_lo
+  // S0, S1 (N each), O0, O1 (N hi and N lo each)
+  static constexpr uint32_t kTmemCols = N == 64 ? 512 : N == 32 ? 256 : 128;
   static constexpr uint32_t kColO = 2 * N;
 };
 
@@ -81,25 +90,29 @@ struct __align__(1024) TreeSmem {
   uint8_t v[S::kStages][S::kTileBytes];
   uint8_t p[S::kPBufs][S::kPBytes];
   uint8_t q[S::kHalves * N * 128];
-  float neg_m[N];   // -m of every draft
-  float alpha[N];   // factors of a growth; at a piece's end the sums
-  int top[N];       // largest scores of a tile, as ordered_int (INT_MIN between growths)
+  float neg_m[N];      // -m of every draft
+  float alpha[N];      // factors of a growth
+  int top[N];          // largest scores of a tile, as ordered_int (INT_MIN between growths)
+  float sums[2][4][N]; // a finished piece's sums, a warp's lanes each, and its m
+  float m[2][N];
+  float inv[N];        // side warps: 1 / sum
   __align__(4) uint8_t depth[N];
   uint64_t q_full, q_free;
   uint64_t k_full[S::kStages], k_empty[S::kStages];
   uint64_t v_full[S::kStages], v_empty[S::kStages];
+  uint64_t v_ask, v_fit;  // a masked tile's V has landed; it is scanned
   uint64_t s_full[2];  // S of a tile finished
-  // P of a tile written, V's copy fit to use (one arrival a softmax warp).  Two,
-  // since the softmax may finish a second tile while the MMA warp still waits for
-  // the first one's V: S of a third tile is only issued after that PV.
+  // P of a tile written (one arrival a softmax warp).  Two, since the softmax may
+  // finish a second tile while the MMA warp still waits for the first one's V: S
+  // of a third tile is only issued after that PV.
   uint64_t p_full[2];
   // O += P V of a tile finished.  Waited for with one tile outstanding at most
   // (S of a tile in hand says that the PV of the tile before the last is done).
   uint64_t pv_done;
-  uint64_t o_done;     // a piece's last PV finished
+  uint64_t o_done[2], o_free[2];  // a piece's last PV finished; its results taken
+  uint64_t l_done[2];  // sums and m of a piece written
   uint64_t turned;     // RoPE: a piece's queries and drafted keys turned
   uint64_t mma_done;
-  uint32_t bad[4];     // rows of the V tile that held a non-finite value
   uint32_t tmem_base;
   int dead;
 };
@@ -109,6 +122,7 @@ struct TreeTcArgs {
   TreeView tv;
   const __nv_bfloat16 *vd, *vc;  // the values, for the ones that are not finite
   __nv_bfloat16 *out;
+  int box_rows;  // of the drafts' tiles
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *err,
@@ -128,7 +142,18 @@ struct PieceTiles {
     const int c1 = min(pc.key_end - 1, (r.held + kTile - 1) / kTile);
     n = drafts + max(0, c1 - c0);
   }
+  // tile j is the drafts', or begins at this slot
+  __device__ __forceinline__ bool is_drafts(int j) const { return drafts && j == 0; }
+  __device__ __forceinline__ int slot(int j) const { return (c0 + j - drafts) * kTile; }
+  // whether some draft may not see some row of tile j
+  __device__ __forceinline__ bool masked(int j, const RingView &r) const {
+    return is_drafts(j) || r.swa || slot(j) + kTile > r.plen;
+  }
 };
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &u, int i) {
+  return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+}
 
 // Byte offset of 16-byte chunk c of row r in a swizzled tile of 64-column
 // blocks of `block` bytes.
@@ -254,7 +279,8 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
   const DeviceView &v = a.v;
   const TreeView &tv = a.tv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kProducer = S::kSoftWarps, kMma = S::kSoftWarps + 1;
+  constexpr int kSide = S::kSoftWarps, kProducer = kSide + 4, kMma = kProducer + 1;
+  const int row0 = (int)blockIdx.y * N;  // this CTA's first draft
   const int p_begin = tv.cta_piece[blockIdx.x], p_end = tv.cta_piece[blockIdx.x + 1];
 
   if (threadIdx.x == 0) {
@@ -269,15 +295,18 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
       mbar_init(&sm.p_full[s], S::kSoftWarps);
+      mbar_init(&sm.o_done[s], 1);
+      mbar_init(&sm.o_free[s], 4);
+      mbar_init(&sm.l_done[s], S::kSoftWarps);
     }
     mbar_init(&sm.pv_done, 1);
-    mbar_init(&sm.o_done, 1);
-    mbar_init(&sm.turned, S::kSoftWarps);
+    mbar_init(&sm.turned, 4);
+    mbar_init(&sm.v_ask, 1);
+    mbar_init(&sm.v_fit, 4);
     mbar_init(&sm.mma_done, 1);
     sm.dead = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x < 4) sm.bad[threadIdx.x] = 0u;
   if (warp == kProducer && lane == 0) {
     // the plan and the maps are the tree's own; the first tiles' way to L2 can
     // begin while the kernel before this one still runs (a hint returns nothing)
@@ -309,27 +338,29 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     // test-only fault injection: no loads at all, so every wait runs out
     const bool drop = (*v.fault & RSWA_FAULT_DROP_DECODE_COPIES) != 0;
     if (lane == 0 && !drop) {
-      constexpr uint32_t kDraftBytes = (uint32_t)N * 128u * kHalves;
+      constexpr uint32_t kQBytes = (uint32_t)N * 128u * kHalves;
+      const uint32_t draft_bytes = (uint32_t)a.box_rows * 128u * kHalves;
       int it = 0, active = 0;
       bool ok = true;
       for (int p = p_begin; ok && p < p_end; ++p) {
         const DecodePiece pc = tv.pieces[p];
-        if (tv.n[pc.b] == 0) continue;
+        if (tv.n[pc.b] <= row0) continue;
         const PieceTiles pt(pc, ring_view(v, pc.b, pc.plen));
         if (pt.n == 0) continue;
         if (!(ok = wait_bar(&sm.q_free, (active & 1) ^ 1, v.err, dead))) break;
         const int xh = pc.h * D, y_draft = pc.b * tv.T;
-        mbar_arrive_expect_tx(&sm.q_full, kDraftBytes);
+        mbar_arrive_expect_tx(&sm.q_full, kQBytes);
         for (int x = 0; x < kHalves; ++x)
-          tc::tma_load_2d(sm.q + x * (N * 128), &tm_q, xh + 64 * x, y_draft, &sm.q_full);
+          tc::tma_load_2d(sm.q + x * (N * 128), &tm_q, xh + 64 * x, y_draft + row0,
+                          &sm.q_full);
         ++active;
         for (int j = 0; j < pt.n; ++j, ++it) {
-          const bool drafts = pt.drafts && j == 0;
+          const bool drafts = pt.is_drafts(j);
           const int s = it % NST;
           const uint32_t parity = ((it / NST) & 1) ^ 1;
-          const uint32_t bytes = drafts ? kDraftBytes : (uint32_t)S::kTileBytes;
+          const uint32_t bytes = drafts ? draft_bytes : (uint32_t)S::kTileBytes;
           const int x0 = drafts ? xh : 0;
-          const int y0 = drafts ? y_draft : (int)(pc.row0 + (int64_t)(pt.c0 + j - pt.drafts) * kTile);
+          const int y0 = drafts ? y_draft : (int)(pc.row0 + pt.slot(j));
           if (!(ok = wait_bar(&sm.k_empty[s], parity, v.err, dead))) break;
           mbar_arrive_expect_tx(&sm.k_full[s], bytes);
           for (int x = 0; x < kHalves; ++x)
@@ -359,25 +390,33 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     if (lane == 0) {
       const uint32_t q_addr = smem_u32(sm.q);
       int it = 0, active = 0;
+      uint32_t scans = 0;
       bool ok = true;
-      auto pv = [&](int i, bool first) {  // O += P V of tile i
+      // O += P V of tile i, the first of its piece or not, into O buffer o
+      auto pv = [&](int i, bool first, bool masked, int o) {
         const int s = i % NST;
         if (!wait_bar(&sm.v_full[s], (i / NST) & 1, v.err, dead)) return false;
+        if (masked) {
+          mbar_arrive(&sm.v_ask);
+          if (!wait_bar(&sm.v_fit, scans++ & 1u, v.err, dead)) return false;
+        }
         if (!wait_bar(&sm.p_full[i & 1], (i >> 1) & 1, v.err, dead)) return false;
         tc::fence_after_sync();
-        issue_pv<D, N>(tbase + S::kColO, smem_u32(sm.p[i % S::kPBufs]), smem_u32(sm.v[s]), !first);
+        issue_pv<D, N>(tbase + S::kColO + (uint32_t)o * (2 * N), smem_u32(sm.p[i % S::kPBufs]),
+                       smem_u32(sm.v[s]), !first);
         tc::commit(&sm.v_empty[s]);
         tc::commit(&sm.pv_done);
         return true;
       };
       for (int p = p_begin; ok && p < p_end; ++p) {
         const DecodePiece pc = tv.pieces[p];
-        if (tv.n[pc.b] == 0) continue;
-        const PieceTiles pt(pc, ring_view(v, pc.b, pc.plen));
+        if (tv.n[pc.b] <= row0) continue;
+        const RingView ring = ring_view(v, pc.b, pc.plen);
+        const PieceTiles pt(pc, ring);
         if (pt.n == 0) continue;
         if (!(ok = wait_bar(&sm.q_full, active & 1, v.err, dead))) break;
         if (v.rope && !(ok = wait_bar(&sm.turned, active & 1, v.err, dead))) break;
-        ++active;
+        const int o = active & 1;
         for (int j = 0; ok && j < pt.n; ++j, ++it) {
           const int s = it % NST;
           if (!(ok = wait_bar(&sm.k_full[s], (it / NST) & 1, v.err, dead))) break;
@@ -387,48 +426,138 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           tc::commit(&sm.s_full[it & 1]);
           tc::commit(&sm.k_empty[s]);
           if (j == pt.n - 1) tc::commit(&sm.q_free);
-          if (j > 0) ok = pv(it - 1, j == 1);
+          if (j == 1 &&  // the results of the piece before the last are out of this O
+              !(ok = wait_bar(&sm.o_free[o], ((active >> 1) & 1) ^ 1, v.err, dead)))
+            break;
+          if (j > 0) ok = pv(it - 1, j == 1, pt.masked(j - 1, ring), o);
         }
-        if (ok && (ok = pv(it - 1, pt.n == 1))) tc::commit(&sm.o_done);
+        if (ok && pt.n == 1) ok = wait_bar(&sm.o_free[o], ((active >> 1) & 1) ^ 1, v.err, dead);
+        if (ok && (ok = pv(it - 1, pt.n == 1, pt.masked(pt.n - 1, ring), o)))
+          tc::commit(&sm.o_done[o]);
+        ++active;
       }
       tc::commit(&sm.mma_done);
       mbar_wait_bounded(&sm.mma_done, 0, v.err, RSWA_DEVERR_TIMEOUT);
     }
-  } else {
-    // --------------------------------------------------------------- softmax
-    constexpr int kAll = S::kSoftWarps * 32;
-    const int group = warp >> 2;
-    const int key = (int)threadIdx.x & 127;     // key row of the tile, and TMEM lane
-    const int col0 = group * NC;                // first draft of this thread
+  } else if (warp >= kSide) {
+    // ------------------------------------------------------------ side warps
+    const int tid = (int)threadIdx.x - kSide * 32;  // 0..127: a row of a tile, a TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_hi = tbase + lane_off + S::kColO + (uint32_t)col0, t_lo = t_hi + N;
     // element of the output on this lane (64 rows of an MMA take 16 lanes a warp)
-    const int elem = D == 128 ? key : (warp & 3) * 16 + (lane & 15);
+    const int elem = D == 128 ? tid : (warp & 3) * 16 + (lane & 15);
     const bool has_elem = D == 128 || lane < 16;
-    const int bar_group = 1 + group;            // hardware barriers: a group's, and 5 for all
-    const float sl2 = v.scale * kLog2e;
-    const uint64_t sl2x2 = tc::f2_pack(sl2, sl2), minus1 = tc::f2_pack(-1.f, -1.f);
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       wait_bar(bar, parity, v.err, dead);
       __syncwarp();
     };
     int it = 0, active = 0;
+    uint32_t scans = 0;
+    int last = -1;            // the piece whose results are due
+    bool last_mend = false;   // a value that is not finite was taken out of its V
+    // The results of piece `last`: final where it is the ring's only one, else a partial.
+    auto finish = [&]() {
+      const DecodePiece pc = tv.pieces[last];
+      const int o = (active - 1) & 1;
+      const uint32_t parity = (uint32_t)((active - 1) >> 1) & 1u;
+      const int n = min(tv.n[pc.b] - row0, N);
+      const int64_t draft0 = (int64_t)pc.b * tv.T + row0;
+      const uint32_t t_hi = tbase + lane_off + S::kColO + (uint32_t)o * (2 * N), t_lo = t_hi + N;
+      wait(&sm.l_done[o], parity);
+      if (tid < N) {
+        const float l = (sm.sums[o][0][tid] + sm.sums[o][1][tid]) +
+                        (sm.sums[o][2][tid] + sm.sums[o][3][tid]);
+        sm.inv[tid] = 1.f / l;
+        if (pc.count > 1 && tid < n) {
+          const float m = sm.m[o][tid];
+          tv.part_ml[(int64_t)last * tv.T + row0 + tid] =
+              make_float2(m == -FLT_MAX ? -INFINITY : m, l);
+        }
+      }
+      __syncwarp();
+      wait(&sm.o_done[o], parity);
+      tc::fence_after_sync();
+      if (last_mend) {
+        // what the scan took out, to the drafts that see it
+        const RingView ring = ring_view(v, pc.b, pc.plen);
+        const PieceTiles pt(pc, ring);
+#pragma unroll 1
+        for (int j = 0; j < pt.n; ++j) {
+          if (!pt.masked(j, ring)) continue;
+          const bool drafts = pt.is_drafts(j);
+          const int held = min(kTile, drafts ? row0 + n : ring.held - pt.slot(j));
+#pragma unroll 1
+          for (int r = 0; r < held; ++r) {
+            const float y = __bfloat162float(
+                drafts ? a.vd[((draft0 - row0 + r) * v.H + pc.h) * D + elem]
+                       : a.vc[(pc.row0 + pt.slot(j) + r) * (int64_t)D + elem]);
+            if (!__any_sync(0xffffffffu, !isfinite(y))) continue;
+            const uint4 below = drafts ? tv.below[draft0 - row0 + r] : make_uint4(0u, 0u, 0u, 0u);
+            const int age = drafts ? 0 : slot_age(ring, pt.slot(j) + r);
+#pragma unroll 1
+            for (int c = 0; c < n; ++c) {
+              const int i = row0 + c;
+              const bool seen = drafts ? ((word_of(below, i >> 5) >> (i & 31)) & 1u) != 0u
+                                       : age <= v.W - 1 - tv.depth[draft0 + c];
+              if (!seen) continue;
+              uint32_t u;
+              tc::ld1(t_hi + (uint32_t)c, &u);
+              tc::wait_ld();
+              if (!isfinite(y)) u = __float_as_uint(__uint_as_float(u) + y);
+              tc::st1(t_hi + (uint32_t)c, u);
+              tc::wait_st();
+            }
+          }
+        }
+      }
+      named_bar_sync(3, 128);  // sm.inv is written
+      const bool whole = pc.count == 1;
+      const int64_t step = whole ? (int64_t)v.H * D : D;  // elements from draft to draft
+      __nv_bfloat16 *dst = a.out + (draft0 * v.H + pc.h) * D + elem;
+      float *part = tv.part_o + ((int64_t)last * tv.T + row0) * D + elem;
+#pragma unroll 1
+      for (int c0 = 0; c0 < n; c0 += 8) {
+        float x[8], x_lo[8];
+        tc::ld8(t_hi + (uint32_t)c0, reinterpret_cast<uint32_t *>(x));
+        tc::ld8(t_lo + (uint32_t)c0, reinterpret_cast<uint32_t *>(x_lo));
+        tc::wait_ld();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] += isfinite(x[c]) ? x_lo[c] : 0.f;
+        const int left = has_elem ? n - c0 : 0;
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < left) dst[c * step] = __float2bfloat16_rn(x[c] * sm.inv[c0 + c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < left) part[c * step] = x[c];
+        }
+        dst += 8 * step;
+        part += 8 * step;
+        __syncwarp();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_free[o]);
+      named_bar_sync(3, 128);  // sm.inv is read
+      last = -1;
+    };
     for (int p = p_begin; p < p_end; ++p) {
       const DecodePiece pc = tv.pieces[p];
       const int n = tv.n[pc.b];
-      if (n == 0) continue;
+      if (n <= row0) continue;
       const RingView ring = ring_view(v, pc.b, pc.plen);
       const PieceTiles pt(pc, ring);
       const int64_t draft0 = (int64_t)pc.b * tv.T;
-      const int tid = (int)threadIdx.x;
       if (pt.n == 0) {  // nothing to see in this piece
-        if (pc.count > 1 && tid < n)
-          tv.part_ml[(int64_t)p * tv.T + tid] = make_float2(-INFINITY, 0.f);
+        if (pc.count > 1 && tid < N && row0 + tid < n)
+          tv.part_ml[(int64_t)p * tv.T + row0 + tid] = make_float2(-INFINITY, 0.f);
         continue;
       }
       if (v.rope) {
         wait(&sm.q_full, active & 1);
-        if (tid < n) turn_row<D>(sm.q, tid, N * 128, tv.cs + (draft0 + tid) * (D / 2));
+        if (tid < N && row0 + tid < n)
+          turn_row<D>(sm.q, tid, N * 128, tv.cs + (draft0 + row0 + tid) * (D / 2));
         if (pt.drafts) {
           wait(&sm.k_full[it % NST], (it / NST) & 1);
           if (tid < n)
@@ -438,33 +567,94 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.turned);
       }
+      bool mend = false;
+      for (int j = 0; j < pt.n; ++j, ++it) {
+        if (pt.masked(j, ring)) {
+          // V's rows that hold no entry become 0, and so do values that are not finite
+          const int held = pt.is_drafts(j) ? n : ring.held - pt.slot(j);
+          bool bad = false;
+          wait(&sm.v_ask, scans++ & 1u);
+          uint8_t *vt = sm.v[it % NST];
+          constexpr int kScan = 8;  // 16-byte chunks of a row looked at together
+          for (int c0 = 0; c0 < D / 8; c0 += kScan) {
+            uint4 u[kScan];
+            uint32_t t = 0;
+#pragma unroll
+            for (int c = 0; c < kScan; ++c)
+              u[c] = *reinterpret_cast<const uint4 *>(vt + chunk_at(tid, c0 + c, kHalfBytes));
+#pragma unroll
+            for (int c = 0; c < kScan; ++c)
+              t |= not_finite(u[c].x) | not_finite(u[c].y) | not_finite(u[c].z) | not_finite(u[c].w);
+            if (tid < held && !t) continue;
+            bad |= tid < held;
+#pragma unroll
+            for (int c = 0; c < kScan; ++c)
+              *reinterpret_cast<uint4 *>(vt + chunk_at(tid, c0 + c, kHalfBytes)) =
+                  tid < held ? make_uint4(finite_part(u[c].x), finite_part(u[c].y),
+                                          finite_part(u[c].z), finite_part(u[c].w))
+                             : make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.v_fit);
+          mend |= bar_red_or(3, 128, bad);
+        }
+        if (j == 0 && last >= 0) finish();
+      }
+      last = p;
+      last_mend = mend;
       ++active;
-      // m starts below every score; a column that holds no draft never grows.  (Each
-      // group's own columns: another may still be at the previous piece's end.)
+    }
+    if (last >= 0) finish();
+  } else {
+    // --------------------------------------------------------------- softmax
+    const int group = warp >> 2;
+    const int key = (int)threadIdx.x & 127;     // key row of the tile, and TMEM lane
+    const int col0 = group * NC;                // first column of this thread
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int bar_group = 1 + group;            // hardware barriers: a group's; 3: the side warps'
+    const float sl2 = v.scale * kLog2e;
+    const uint64_t sl2x2 = tc::f2_pack(sl2, sl2), minus1 = tc::f2_pack(-1.f, -1.f);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      wait_bar(bar, parity, v.err, dead);
+      __syncwarp();
+    };
+    int it = 0, active = 0;
+    for (int p = p_begin; p < p_end; ++p) {
+      const DecodePiece pc = tv.pieces[p];
+      const int n_all = tv.n[pc.b], n = min(n_all - row0, N);
+      if (n <= 0) continue;
+      const RingView ring = ring_view(v, pc.b, pc.plen);
+      const PieceTiles pt(pc, ring);
+      if (pt.n == 0) continue;
+      const int64_t draft0 = (int64_t)pc.b * tv.T;
+      const int o = active & 1;
+      const uint32_t t_hi =
+          tbase + lane_off + S::kColO + (uint32_t)o * (2 * N) + (uint32_t)col0;
+      const uint32_t t_lo = t_hi + N;
+      named_bar_sync(bar_group, 128);  // the previous piece's m is read
+      // m starts below every score; a column that holds no draft never grows
       if (key < NC) {
         const int c = col0 + key;
         sm.neg_m[c] = c < n ? FLT_MAX : -FLT_MAX;
         sm.top[c] = INT_MIN;
-        sm.depth[c] = (uint8_t)(c < n ? tv.depth[draft0 + c] : 0);
+        sm.depth[c] = (uint8_t)(c < n ? tv.depth[draft0 + row0 + c] : 0);
       }
       __syncwarp();
-      named_bar_sync(5, kAll);
+      named_bar_sync(bar_group, 128);
       uint64_t l2[NC / 2];  // sums of weights over this lane's keys
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) l2[c] = 0;
 
       for (int j = 0; j < pt.n; ++j, ++it) {
-        const bool drafts = pt.drafts && j == 0;
-        const int k0 = drafts ? 0 : (pt.c0 + j - pt.drafts) * kTile;  // first draft / slot
-        const bool masked = drafts || ring.swa || k0 + kTile > ring.plen;
+        const bool masked = pt.masked(j, ring);
         const uint32_t t_s = tbase + lane_off + (uint32_t)(it & 1) * N + (uint32_t)col0;
-        uint32_t sees = 0xffffffffu;  // bit c: draft col0 + c sees this key
+        uint32_t sees = 0xffffffffu;  // bit c: draft row0 + col0 + c sees this key
         if (masked) {
-          if (drafts) {
-            const uint4 u = key < n ? tv.below[draft0 + key] : make_uint4(0u, 0u, 0u, 0u);
-            sees = group == 0 ? u.x : group == 1 ? u.y : group == 2 ? u.z : u.w;
+          if (pt.is_drafts(j)) {
+            sees = key < n_all ? word_of(tv.below[draft0 + key], (row0 + col0) >> 5) : 0u;
           } else {
-            const int age = slot_age(ring, k0 + key);
+            const int age = slot_age(ring, pt.slot(j) + key);
             const int deepest = age == INT_MIN ? INT_MAX : age == INT_MAX ? -1 : v.W - 1 - age;
             if (deepest >= RSWA_TREE_MAX || deepest < 0) {
               sees = deepest < 0 ? 0u : 0xffffffffu;
@@ -567,136 +757,25 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           *reinterpret_cast<uint4 *>(pt_row + chunk_at(key, (N + col0 + c) / 8, kHalfBytes)) =
               make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        bool mend = false;
-        if (masked) {
-          // V's rows that hold no entry become 0, and so do values that are not finite
-          const int held = drafts ? n : ring.held - k0;
-          bool bad = false;
-          wait(&sm.v_full[it % NST], (it / NST) & 1);
-          uint8_t *vt = sm.v[it % NST];
-          constexpr int kMine = D / 8 / S::kGroups;  // this group's chunks of the row
-          constexpr int kScan = kMine < 8 ? kMine : 8;  // loaded together
-          static_assert(kMine % kScan == 0, "whole batches");
-          for (int c0 = group * kMine; c0 < (group + 1) * kMine; c0 += kScan) {
-            uint4 u[kScan];
-            uint32_t t = 0;
-#pragma unroll
-            for (int c = 0; c < kScan; ++c)
-              u[c] = *reinterpret_cast<const uint4 *>(vt + chunk_at(key, c0 + c, kHalfBytes));
-#pragma unroll
-            for (int c = 0; c < kScan; ++c)
-              t |= not_finite(u[c].x) | not_finite(u[c].y) | not_finite(u[c].z) | not_finite(u[c].w);
-            if (key < held && !t) continue;
-            bad |= key < held;
-#pragma unroll
-            for (int c = 0; c < kScan; ++c)
-              *reinterpret_cast<uint4 *>(vt + chunk_at(key, c0 + c, kHalfBytes)) =
-                  key < held ? make_uint4(finite_part(u[c].x), finite_part(u[c].y),
-                                          finite_part(u[c].z), finite_part(u[c].w))
-                             : make_uint4(0u, 0u, 0u, 0u);
-          }
-          __syncwarp();
-          mend = bar_red_or(5, kAll, bad);
-          if (mend) {
-            const uint32_t word = __ballot_sync(0xffffffffu, bad);
-            if (lane == 0) atomicOr(&sm.bad[warp & 3], word);
-          }
-        }
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[it & 1]);
-        if (mend) {
-          // O of this tile, then the values taken out of it
-          if (it > 0) wait(&sm.pv_done, (it - 1) & 1);
-          wait(&sm.pv_done, it & 1);
-          tc::fence_after_sync();
-          named_bar_sync(5, kAll);  // sm.bad is written
-#pragma unroll 1
-          for (int r = 0; r < kTile; ++r) {
-            if (!((sm.bad[r >> 5] >> (r & 31)) & 1u)) continue;
-            const float y = __bfloat162float(
-                drafts ? a.vd[((draft0 + r) * v.H + pc.h) * D + elem]
-                       : a.vc[(pc.row0 + k0 + r) * (int64_t)D + elem]);
-            const int age = drafts ? 0 : slot_age(ring, k0 + r);
-#pragma unroll 1
-            for (int c = 0; c < NC && col0 + c < n; ++c) {
-              bool seen;
-              if (drafts) {
-                const uint4 u = tv.below[draft0 + r];
-                const uint32_t w = group == 0 ? u.x : group == 1 ? u.y : group == 2 ? u.z : u.w;
-                seen = ((w >> c) & 1u) != 0u;
-              } else {
-                seen = age <= v.W - 1 - sm.depth[col0 + c];
-              }
-              if (!seen) continue;
-              uint32_t u;
-              tc::ld1(t_hi + (uint32_t)c, &u);
-              tc::wait_ld();
-              if (!isfinite(y)) u = __float_as_uint(__uint_as_float(u) + y);
-              tc::st1(t_hi + (uint32_t)c, u);
-              tc::wait_st();
-            }
-          }
-          tc::fence_before_sync();
-          named_bar_sync(5, kAll);  // sm.bad is read
-          if (threadIdx.x < 4) sm.bad[threadIdx.x] = 0u;
-          __syncwarp();
-        }
       }
-      // the piece's result: final where it is the ring's only one, else a partial
-      wait(&sm.o_done, (active - 1) & 1);
-      tc::fence_after_sync();
-      {
-        float sum[NC];
+      // sums and m to the side warps
+      float sum[NC];
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c) {
-          sum[2 * c] = tc::f2_lo(l2[c]);
-          sum[2 * c + 1] = tc::f2_hi(l2[c]);
-        }
-        reduce_lanes<NC>(sum, lane, [](float a, float b) { return a + b; });
-        float *red = reinterpret_cast<float *>(sm.p[0]) + group * (4 * NC);
-        red[(warp & 3) * NC + lane * NC / 32] = sum[0];
-        __syncwarp();
-        named_bar_sync(bar_group, 128);
-        if (key < NC) {
-          const float l = (red[key] + red[NC + key]) + (red[2 * NC + key] + red[3 * NC + key]);
-          sm.alpha[col0 + key] = 1.f / l;
-          if (pc.count > 1 && col0 + key < n) {
-            const float m = -sm.neg_m[col0 + key];
-            tv.part_ml[(int64_t)p * tv.T + col0 + key] =
-                make_float2(m == -FLT_MAX ? -INFINITY : m, l);
-          }
-        }
-        __syncwarp();
-        named_bar_sync(bar_group, 128);
+      for (int c = 0; c < NC / 2; ++c) {
+        sum[2 * c] = tc::f2_lo(l2[c]);
+        sum[2 * c + 1] = tc::f2_hi(l2[c]);
       }
-      const bool whole = pc.count == 1;
-      __nv_bfloat16 *dst = a.out + ((draft0 + col0) * v.H + pc.h) * D + elem;
-      float *part = tv.part_o + ((int64_t)p * tv.T + col0) * D + elem;
-      const int row_step = v.H * D;
-#pragma unroll 1
-      for (int c0 = 0; c0 < NC && col0 + c0 < n; c0 += 8) {
-        float o[8], o_lo[8];
-        tc::ld8(t_hi + (uint32_t)c0, reinterpret_cast<uint32_t *>(o));
-        tc::ld8(t_lo + (uint32_t)c0, reinterpret_cast<uint32_t *>(o_lo));
-        tc::wait_ld();
-        if (has_elem) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (isfinite(o[c])) o[c] += o_lo[c];
-            if (col0 + c0 + c < n) {
-              if (whole)
-                dst[c * row_step] = __float2bfloat16_rn(o[c] * sm.alpha[col0 + c0 + c]);
-              else
-                part[c * D] = o[c];
-            }
-          }
-        }
-        __syncwarp();
-        dst += 8 * row_step;
-        part += 8 * D;
-      }
+      reduce_lanes<NC>(sum, lane, [](float a, float b) { return a + b; });
+      wait(&sm.o_free[o], ((active >> 1) & 1) ^ 1);  // those of two pieces ago are read
+      sm.sums[o][warp & 3][col0 + lane * NC / 32] = sum[0];
+      if (key < NC) sm.m[o][col0 + key] = -sm.neg_m[col0 + key];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.l_done[o]);
+      ++active;
     }
   }
 
@@ -721,13 +800,14 @@ cudaError_t launch_t(const DeviceView &v, const TreeView &tv, const CUtensorMap 
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   const int64_t rows = (int64_t)v.B * tv.T, elems = (int64_t)v.H * D;
+  const int box_rows = (tv.T + 7) / 8 * 8;  // whole 8-row swizzle atoms
   CUtensorMap tq, tk, tvv;
-  if (!make_tmap_rows(&tq, q, rows, elems, N) || !make_tmap_rows(&tk, kd, rows, elems, N) ||
-      !make_tmap_rows(&tvv, vd, rows, elems, N))
+  if (!make_tmap_rows(&tq, q, rows, elems, N) || !make_tmap_rows(&tk, kd, rows, elems, box_rows) ||
+      !make_tmap_rows(&tvv, vd, rows, elems, box_rows))
     return cudaErrorInvalidValue;
   const TreeTcArgs args{v, tv, (const __nv_bfloat16 *)vd, (const __nv_bfloat16 *)vc,
-                        (__nv_bfloat16 *)out};
-  return launch_overlapped(tree_tc_kernel<D, N>, dim3((unsigned)tv.grid),
+                        (__nv_bfloat16 *)out, box_rows};
+  return launch_overlapped(tree_tc_kernel<D, N>, dim3((unsigned)tv.grid, (unsigned)((tv.T + N - 1) / N)),
                            dim3(Shape<D, N>::kThreads), (size_t)smem, s, tq, tk, tvv, tkc, tvc, args);
 }
 
@@ -737,8 +817,7 @@ cudaError_t launch_d(const DeviceView &v, const TreeView &tv, const CUtensorMap 
                      const void *vc, void *out, cudaStream_t s) {
   if (tv.T <= 16) return launch_t<D, 16>(v, tv, tkc, tvc, q, kd, vd, vc, out, s);
   if (tv.T <= 32) return launch_t<D, 32>(v, tv, tkc, tvc, q, kd, vd, vc, out, s);
-  if (tv.T <= 64) return launch_t<D, 64>(v, tv, tkc, tvc, q, kd, vd, vc, out, s);
-  return launch_t<D, 128>(v, tv, tkc, tvc, q, kd, vd, vc, out, s);
+  return launch_t<D, 64>(v, tv, tkc, tvc, q, kd, vd, vc, out, s);
 }
 
 }  // namespace
