@@ -265,43 +265,77 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // The tiles of all rings (each ring's draft tiles, then its cache tiles) cut
-// into equal ranges, one per CTA.
-DecodePlan plan_tree(const rswa_state *s, int T, int tile, int ctas) {
+// into ranges of about equal cost, one per CTA.  Beginning and ending a piece of
+// a ring costs a CTA as much as `piece_cost` tiles, so the pieces count too: the
+// cut is the one with the least cost that some CTA has, found by bisection.
+struct TreeCut {
+  const rswa_state *s;
+  int64_t draft_tiles;
+  int tile, piece_cost;
+
+  int64_t tiles(int b) const {
+    return draft_tiles + (s->plen[(size_t)b] + s->cfg.window + tile - 1) / tile;
+  }
+  // CTAs that ranges of at most `budget` (> piece_cost) take; on_piece(b, h, t0, t1, cta).
+  template <typename F>
+  int64_t run(int64_t budget, F on_piece) const {
+    int64_t cta = 0, left = budget;
+    for (int b = 0; b < s->cfg.batch; ++b) {
+      const int64_t n = tiles(b);
+      for (int h = 0; h < s->cfg.num_heads; ++h)
+        for (int64_t t0 = 0; t0 < n;) {
+          if (left <= piece_cost) {
+            ++cta;
+            left = budget;
+          }
+          const int64_t t1 = std::min(n, t0 + left - piece_cost);
+          on_piece(b, h, t0, t1, cta);
+          left -= piece_cost + (t1 - t0);
+          t0 = t1;
+        }
+    }
+    return cta + 1;
+  }
+};
+
+DecodePlan plan_tree(const rswa_state *s, int T, int tile, int ctas, int piece_cost) {
   const int B = s->cfg.batch, H = s->cfg.num_heads, W = s->cfg.window;
-  const int64_t draft_tiles = (T + tile - 1) / tile;
+  const TreeCut cut{s, (T + tile - 1) / tile, tile, piece_cost};
   int64_t total = 0;
-  for (int b = 0; b < B; ++b) total += H * (draft_tiles + (s->plen[(size_t)b] + W + tile - 1) / tile);
-  const int64_t per = std::max<int64_t>(1, (total + ctas - 1) / ctas);
+  for (int b = 0; b < B; ++b) total += H * (cut.tiles(b) + piece_cost);
+  auto nothing = [](int, int, int64_t, int64_t, int64_t) {};
+  int64_t lo = piece_cost + 1, hi = std::max(lo, total);  // hi: one CTA holds all
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (cut.run(mid, nothing) <= ctas)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
   DecodePlan p;
   p.bh_piece.reserve((size_t)B * H + 1);
-  int64_t done = 0;  // tiles handed out so far
-  for (int b = 0; b < B; ++b) {
+  int64_t first = 0;
+  cut.run(hi, [&](int b, int h, int64_t t0, int64_t t1, int64_t cta) {
     const int64_t P = s->plen[(size_t)b];
-    const int64_t tiles = draft_tiles + (P + W + tile - 1) / tile;
-    for (int h = 0; h < H; ++h) {
-      const size_t first = p.pieces.size();
+    if (t0 == 0) {
+      first = (int64_t)p.pieces.size();
       p.bh_piece.push_back((int32_t)first);
-      for (int64_t t0 = 0; t0 < tiles;) {
-        const int64_t cta = done / per;
-        const int64_t t1 = std::min(tiles, t0 + (cta + 1) * per - done);
-        while ((int64_t)p.cta_piece.size() <= cta) p.cta_piece.push_back((int32_t)p.pieces.size());
-        DecodePiece pc;
-        pc.row0 = (int64_t)H * s->slot_base[(size_t)b] + (int64_t)h * (P + W);
-        pc.b = b;
-        pc.h = h;
-        pc.key_begin = (int32_t)t0;
-        pc.key_end = (int32_t)t1;
-        pc.plen = (int32_t)P;
-        pc.first = (int32_t)first;
-        pc.cta = (int32_t)cta;
-        p.pieces.push_back(pc);
-        done += t1 - t0;
-        t0 = t1;
-      }
-      for (size_t i = first; i < p.pieces.size(); ++i)
-        p.pieces[i].count = (int32_t)(p.pieces.size() - first);
     }
-  }
+    while ((int64_t)p.cta_piece.size() <= cta) p.cta_piece.push_back((int32_t)p.pieces.size());
+    DecodePiece pc;
+    pc.row0 = (int64_t)H * s->slot_base[(size_t)b] + (int64_t)h * (P + W);
+    pc.b = b;
+    pc.h = h;
+    pc.key_begin = (int32_t)t0;
+    pc.key_end = (int32_t)t1;
+    pc.plen = (int32_t)P;
+    pc.first = (int32_t)first;
+    pc.cta = (int32_t)cta;
+    p.pieces.push_back(pc);
+    if (t1 == cut.tiles(b))
+      for (size_t i = (size_t)first; i < p.pieces.size(); ++i)
+        p.pieces[i].count = (int32_t)(p.pieces.size() - (size_t)first);
+  });
   p.n_pieces = (int)p.pieces.size();
   p.grid = (int)p.cta_piece.size();
   p.cta_piece.push_back(p.n_pieces);
@@ -313,9 +347,10 @@ DecodePlan plan_for(const rswa_state *s, int T) {
   if (s->cfg.dtype == RSWA_BF16) {
     // the tensor-core kernel: one CTA an SM for every kTreeTcRows drafts
     const int cols = (T + kTreeTcRows - 1) / kTreeTcRows;
-    return plan_tree(s, T, kTreeTcTile, std::max(1, s->num_sms / cols));
+    return plan_tree(s, T, kTreeTcTile, std::max(1, s->num_sms / cols), kTreeTcPieceCost);
   }
-  return plan_tree(s, T, kTreeSimtTile, s->num_sms * tree_simt_ctas_per_sm(s->cfg.head_dim, T));
+  return plan_tree(s, T, kTreeSimtTile, s->num_sms * tree_simt_ctas_per_sm(s->cfg.head_dim, T),
+                   0);
 }
 
 struct TreeLayout {

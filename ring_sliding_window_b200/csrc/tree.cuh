@@ -30,7 +30,10 @@ __device__ __forceinline__ RingView ring_view(const DeviceView &v, int b, int pl
   r.t = v.t[b];
   r.swa = v.swa != 0;
   r.held = plen + (int)(r.t < v.W ? r.t : (int64_t)v.W);
-  r.newest = r.t > 0 ? (int)((r.t - 1) % v.W) : 0;
+  // (32-bit division where it will do: this stands at the head of every piece)
+  r.newest = r.t <= 0 ? 0
+             : r.t <= INT_MAX ? (int)((uint32_t)(r.t - 1) % (uint32_t)v.W)
+                              : (int)((r.t - 1) % v.W);
   const int64_t lo = (int64_t)plen + r.t - v.W + 1;
   r.lo = !r.swa || lo < 0 ? 0 : (lo > plen ? plen : (int)lo);
   return r;

@@ -17,7 +17,7 @@
 //   MMA warp        one thread: S^T = K Q^T (128 keys x N drafts) into one of
 //                   two TMEM buffers, a tile ahead of O^T += V^T P;
 //   softmax warps   thread r of four warps owns key r of the tile (TMEM lane r)
-//                   and up to 32 drafts: 4 warps, or 8 for N = 64;
+//                   and 16 drafts (32 for N = 64): 4, 8 or 8 warps;
 //   4 side warps    what would hold the softmax up where pieces begin and end:
 //                   the scan of V (below), RoPE, and the results of a piece,
 //                   while the next one already fills the other O.
@@ -67,17 +67,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int N>
 struct Shape {
-  static constexpr int kGroups = N <= 32 ? 1 : N / 32;  // of 4 softmax warps
-  static constexpr int NC = N / kGroups;                // drafts of a softmax thread
+  static constexpr int NC = N == 64 ? 32 : 16; // drafts of a softmax thread
+  static constexpr int kGroups = N / NC;       // of 4 softmax warps
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kThreads = (kSoftWarps + 6) * 32;
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kHalfBytes;
   static constexpr int kPBytes = N <= 32 ? kHalfBytes : N / 32 * kHalfBytes;
-  // K and V tiles in flight: 192 KB of them for few drafts, 128 KB beside the
-  // larger P; P twice where it fits
-  static constexpr int kStages = (N <= 32 ? 3 : 2) * (D == 64 ? 2 : 1);
-  static constexpr int kPBufs = N == 64 ? 2 : 1;
+  // K and V tiles in flight, P and Q buffers: what 227 KB hold.  At N = 32 a third
+  // V tile is worth more than a second P and Q (1,088-token prompts of 32 users: 58
+  // against 69 us); at N = 64 a second P more than a second Q.
+  static constexpr int kK = (N <= 32 ? 3 : 2) * (D == 64 ? 2 : 1);
+  static constexpr int kV = (N == 32 ? 3 : 2) * (D == 64 ? 2 : 1);
+  static constexpr int kPBufs = N == 32 ? 1 : 2;
+  static constexpr int kQBufs = N == 16 ? 2 : 1;
   // S0, S1 (N each), O0, O1 (N hi and N lo each)
   static constexpr uint32_t kTmemCols = N == 64 ? 512 : N == 32 ? 256 : 128;
   static constexpr uint32_t kColO = 2 * N;
@@ -86,10 +89,10 @@ struct Shape {
 template <int D, int N>
 struct __align__(1024) TreeSmem {
   using S = Shape<D, N>;
-  uint8_t k[S::kStages][S::kTileBytes];
-  uint8_t v[S::kStages][S::kTileBytes];
+  uint8_t k[S::kK][S::kTileBytes];
+  uint8_t v[S::kV][S::kTileBytes];
   uint8_t p[S::kPBufs][S::kPBytes];
-  uint8_t q[S::kHalves * N * 128];
+  uint8_t q[S::kQBufs][S::kHalves * N * 128];
   float neg_m[N];      // -m of every draft
   float alpha[N];      // factors of a growth
   int top[N];          // largest scores of a tile, as ordered_int (INT_MIN between growths)
@@ -97,10 +100,10 @@ struct __align__(1024) TreeSmem {
   float m[2][N];
   float inv[N];        // side warps: 1 / sum
   __align__(4) uint8_t depth[N];
-  uint64_t q_full, q_free;
-  uint64_t k_full[S::kStages], k_empty[S::kStages];
-  uint64_t v_full[S::kStages], v_empty[S::kStages];
-  uint64_t v_ask, v_fit;  // a masked tile's V has landed; it is scanned
+  uint64_t q_full[S::kQBufs], q_free[S::kQBufs];
+  uint64_t k_full[S::kK], k_empty[S::kK];
+  uint64_t v_full[S::kV], v_empty[S::kV];
+  uint64_t v_ask[S::kV], v_fit[S::kV];  // a masked tile's V is on its way; it is scanned
   uint64_t s_full[2];  // S of a tile finished
   // P of a tile written (one arrival a softmax warp).  Two, since the softmax may
   // finish a second tile while the MMA warp still waits for the first one's V: S
@@ -185,11 +188,11 @@ __device__ __forceinline__ void turn_row(uint8_t *tile, int r, uint32_t block, c
 
 // S^T = K Q^T (128 keys x N drafts).
 template <int D, int N>
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint32_t k_addr) {
+__device__ __forceinline__ void issue_qk(uint32_t elected, uint32_t d_tmem, uint32_t q_addr, uint32_t k_addr) {
   constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, N, false, false);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
-    tc::mma_ss(d_tmem,
+    tc::mma_ss_elected(elected, d_tmem,
                tc::sw128_desc(k_addr + (uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32,
                               16, 1024),
                tc::sw128_desc(q_addr + (uint32_t)(kk >> 2) * (N * 128) + (uint32_t)(kk & 3) * 32,
@@ -199,12 +202,12 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint3
 
 // O^T += V^T P (D elements x (N hi, N lo) drafts, K = 128 keys).
 template <int D, int N>
-__device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_addr, uint32_t v_addr,
+__device__ __forceinline__ void issue_pv(uint32_t elected, uint32_t o_tmem, uint32_t p_addr, uint32_t v_addr,
                                          bool accumulate) {
   constexpr uint32_t idesc = tc::idesc_bf16_f32(D, 2 * N, true, true);
 #pragma unroll
   for (int kk = 0; kk < kTile / 16; ++kk)
-    tc::mma_ss(o_tmem, tc::sw128_desc(v_addr + (uint32_t)kk * 2048, kHalfBytes, 1024),
+    tc::mma_ss_elected(elected, o_tmem, tc::sw128_desc(v_addr + (uint32_t)kk * 2048, kHalfBytes, 1024),
                tc::sw128_desc(p_addr + (uint32_t)kk * 2048, kHalfBytes, 1024), idesc,
                accumulate || kk > 0);
 }
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
                    const __grid_constant__ CUtensorMap tm_vd, const __grid_constant__ CUtensorMap tm_kc,
                    const __grid_constant__ CUtensorMap tm_vc, const TreeTcArgs a) {
   using S = Shape<D, N>;
-  constexpr int NST = S::kStages, NC = S::NC, kHalves = S::kHalves;
+  constexpr int NK = S::kK, NV = S::kV, NQ = S::kQBufs, NC = S::NC, kHalves = S::kHalves;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // dynamic shared memory is only 16-byte aligned: round up to 1024 for the swizzle atoms
   TreeSmem<D, N> &sm = *reinterpret_cast<TreeSmem<D, N> *>(
@@ -284,13 +287,19 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
   const int p_begin = tv.cta_piece[blockIdx.x], p_end = tv.cta_piece[blockIdx.x + 1];
 
   if (threadIdx.x == 0) {
-    mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_free, 1);
-    for (int s = 0; s < NST; ++s) {
+    for (int s = 0; s < NQ; ++s) {
+      mbar_init(&sm.q_full[s], 1);
+      mbar_init(&sm.q_free[s], 1);
+    }
+    for (int s = 0; s < NK; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
       mbar_init(&sm.v_full[s], 1);
       mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.v_ask[s], 1);
+      mbar_init(&sm.v_fit[s], 4);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
@@ -301,8 +310,6 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     }
     mbar_init(&sm.pv_done, 1);
     mbar_init(&sm.turned, 4);
-    mbar_init(&sm.v_ask, 1);
-    mbar_init(&sm.v_fit, 4);
     mbar_init(&sm.mma_done, 1);
     sm.dead = 0;
     fence_mbar_init();
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     tc::prefetch_tmap(&tm_kc);
     tc::prefetch_tmap(&tm_vc);
     const int first = max(0, pc.key_begin - 1);
-    for (int t = first; t < min(pc.key_end - 1, first + NST); ++t)
+    for (int t = first; t < min(pc.key_end - 1, first + NV); ++t)
       for (int x = 0; x < kHalves; ++x) {
         tc::tma_prefetch_2d(&tm_kc, 64 * x, (int)(pc.row0 + (int64_t)t * kTile));
         tc::tma_prefetch_2d(&tm_vc, 64 * x, (int)(pc.row0 + (int64_t)t * kTile));
@@ -345,102 +352,109 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
       for (int p = p_begin; ok && p < p_end; ++p) {
         const DecodePiece pc = tv.pieces[p];
         if (tv.n[pc.b] <= row0) continue;
-        const PieceTiles pt(pc, ring_view(v, pc.b, pc.plen));
-        if (pt.n == 0) continue;
-        if (!(ok = wait_bar(&sm.q_free, (active & 1) ^ 1, v.err, dead))) break;
-        const int xh = pc.h * D, y_draft = pc.b * tv.T;
-        mbar_arrive_expect_tx(&sm.q_full, kQBytes);
-        for (int x = 0; x < kHalves; ++x)
-          tc::tma_load_2d(sm.q + x * (N * 128), &tm_q, xh + 64 * x, y_draft + row0,
-                          &sm.q_full);
-        ++active;
-        for (int j = 0; j < pt.n; ++j, ++it) {
-          const bool drafts = pt.is_drafts(j);
-          const int s = it % NST;
-          const uint32_t parity = ((it / NST) & 1) ^ 1;
-          const uint32_t bytes = drafts ? draft_bytes : (uint32_t)S::kTileBytes;
-          const int x0 = drafts ? xh : 0;
-          const int y0 = drafts ? y_draft : (int)(pc.row0 + pt.slot(j));
-          if (!(ok = wait_bar(&sm.k_empty[s], parity, v.err, dead))) break;
-          mbar_arrive_expect_tx(&sm.k_full[s], bytes);
-          for (int x = 0; x < kHalves; ++x)
-            tc::tma_load_2d(sm.k[s] + x * kHalfBytes, drafts ? &tm_kd : &tm_kc, x0 + 64 * x, y0,
-                            &sm.k_full[s]);
-          if (!(ok = wait_bar(&sm.v_empty[s], parity, v.err, dead))) {
-            mbar_wait_bounded(&sm.k_full[s], (it / NST) & 1, v.err, RSWA_DEVERR_TIMEOUT);
-            break;
-          }
-          mbar_arrive_expect_tx(&sm.v_full[s], bytes);
-          for (int x = 0; x < kHalves; ++x)
-            tc::tma_load_2d(sm.v[s] + x * kHalfBytes, drafts ? &tm_vd : &tm_vc, x0 + 64 * x, y0,
-                            &sm.v_full[s]);
-        }
-      }
-      // every load issued has landed before the CTA may exit (bounded)
-      if (active > 0)
-        mbar_wait_bounded(&sm.q_full, (active - 1) & 1, v.err, RSWA_DEVERR_TIMEOUT);
-      for (int s = 0; s < NST && s < it; ++s) {
-        const int last = s + ((it - 1 - s) / NST) * NST;
-        mbar_wait_bounded(&sm.k_full[s], (last / NST) & 1, v.err, RSWA_DEVERR_TIMEOUT);
-        mbar_wait_bounded(&sm.v_full[s], (last / NST) & 1, v.err, RSWA_DEVERR_TIMEOUT);
-      }
-    }
-  } else if (warp == kMma) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t q_addr = smem_u32(sm.q);
-      int it = 0, active = 0;
-      uint32_t scans = 0;
-      bool ok = true;
-      // O += P V of tile i, the first of its piece or not, into O buffer o
-      auto pv = [&](int i, bool first, bool masked, int o) {
-        const int s = i % NST;
-        if (!wait_bar(&sm.v_full[s], (i / NST) & 1, v.err, dead)) return false;
-        if (masked) {
-          mbar_arrive(&sm.v_ask);
-          if (!wait_bar(&sm.v_fit, scans++ & 1u, v.err, dead)) return false;
-        }
-        if (!wait_bar(&sm.p_full[i & 1], (i >> 1) & 1, v.err, dead)) return false;
-        tc::fence_after_sync();
-        issue_pv<D, N>(tbase + S::kColO + (uint32_t)o * (2 * N), smem_u32(sm.p[i % S::kPBufs]),
-                       smem_u32(sm.v[s]), !first);
-        tc::commit(&sm.v_empty[s]);
-        tc::commit(&sm.pv_done);
-        return true;
-      };
-      for (int p = p_begin; ok && p < p_end; ++p) {
-        const DecodePiece pc = tv.pieces[p];
-        if (tv.n[pc.b] <= row0) continue;
         const RingView ring = ring_view(v, pc.b, pc.plen);
         const PieceTiles pt(pc, ring);
         if (pt.n == 0) continue;
-        if (!(ok = wait_bar(&sm.q_full, active & 1, v.err, dead))) break;
-        if (v.rope && !(ok = wait_bar(&sm.turned, active & 1, v.err, dead))) break;
-        const int o = active & 1;
-        for (int j = 0; ok && j < pt.n; ++j, ++it) {
-          const int s = it % NST;
-          if (!(ok = wait_bar(&sm.k_full[s], (it / NST) & 1, v.err, dead))) break;
-          tc::fence_after_sync();
-          // overwrites S of tile it - 2, which the softmax had read before its PV
-          issue_qk<D, N>(tbase + (uint32_t)(it & 1) * N, q_addr, smem_u32(sm.k[s]));
-          tc::commit(&sm.s_full[it & 1]);
-          tc::commit(&sm.k_empty[s]);
-          if (j == pt.n - 1) tc::commit(&sm.q_free);
-          if (j == 1 &&  // the results of the piece before the last are out of this O
-              !(ok = wait_bar(&sm.o_free[o], ((active >> 1) & 1) ^ 1, v.err, dead)))
-            break;
-          if (j > 0) ok = pv(it - 1, j == 1, pt.masked(j - 1, ring), o);
-        }
-        if (ok && pt.n == 1) ok = wait_bar(&sm.o_free[o], ((active >> 1) & 1) ^ 1, v.err, dead);
-        if (ok && (ok = pv(it - 1, pt.n == 1, pt.masked(pt.n - 1, ring), o)))
-          tc::commit(&sm.o_done[o]);
+        const int qs = active % NQ;
+        if (!(ok = wait_bar(&sm.q_free[qs], ((active / NQ) & 1) ^ 1, v.err, dead))) break;
+        const int xh = pc.h * D, y_draft = pc.b * tv.T;
+        mbar_arrive_expect_tx(&sm.q_full[qs], kQBytes);
+        for (int x = 0; x < kHalves; ++x)
+          tc::tma_load_2d(sm.q[qs] + x * (N * 128), &tm_q, xh + 64 * x, y_draft + row0,
+                          &sm.q_full[qs]);
         ++active;
+        for (int j = 0; j < pt.n; ++j, ++it) {
+          const bool drafts = pt.is_drafts(j);
+          const int ks = it % NK, vs = it % NV;
+          const uint32_t bytes = drafts ? draft_bytes : (uint32_t)S::kTileBytes;
+          const int x0 = drafts ? xh : 0;
+          const int y0 = drafts ? y_draft : (int)(pc.row0 + pt.slot(j));
+          if (!(ok = wait_bar(&sm.k_empty[ks], ((it / NK) & 1) ^ 1, v.err, dead))) break;
+          mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
+          for (int x = 0; x < kHalves; ++x)
+            tc::tma_load_2d(sm.k[ks] + x * kHalfBytes, drafts ? &tm_kd : &tm_kc, x0 + 64 * x, y0,
+                            &sm.k_full[ks]);
+          if (!(ok = wait_bar(&sm.v_empty[vs], ((it / NV) & 1) ^ 1, v.err, dead))) {
+            mbar_wait_bounded(&sm.k_full[ks], (it / NK) & 1, v.err, RSWA_DEVERR_TIMEOUT);
+            break;
+          }
+          mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
+          for (int x = 0; x < kHalves; ++x)
+            tc::tma_load_2d(sm.v[vs] + x * kHalfBytes, drafts ? &tm_vd : &tm_vc, x0 + 64 * x, y0,
+                            &sm.v_full[vs]);
+          if (pt.masked(j, ring)) mbar_arrive(&sm.v_ask[vs]);
+        }
       }
-      tc::commit(&sm.mma_done);
-      mbar_wait_bounded(&sm.mma_done, 0, v.err, RSWA_DEVERR_TIMEOUT);
+      // every load issued has landed before the CTA may exit (bounded): phase of
+      // the last use of slot s among n uses of a ring of slots
+      auto drain = [&](uint64_t *bar, int slots, int n) {
+        for (int s = 0; s < slots && s < n; ++s)
+          mbar_wait_bounded(&bar[s], ((n - 1 - s) / slots) & 1, v.err, RSWA_DEVERR_TIMEOUT);
+      };
+      drain(sm.q_full, NQ, active);
+      drain(sm.k_full, NK, it);
+      drain(sm.v_full, NV, it);
     }
+  } else if (warp == kMma) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t el = tc::elect_one();
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_bar(bar, parity, v.err, dead)) != 0;
+    };
+    int it = 0, active = 0;
+    uint32_t fit = 0;  // bit s: parity of V slot s's next v_fit
+    bool ok = true;
+    // O += P V of tile i, the first of its piece or not, into O buffer o
+    auto pv = [&](int i, bool first, bool masked, int o) {
+      const int s = i % NV;
+      if (!wait(&sm.v_full[s], (i / NV) & 1)) return false;
+      if (masked) {
+        if (!wait(&sm.v_fit[s], (fit >> s) & 1u)) return false;
+        fit ^= 1u << s;
+      }
+      if (!wait(&sm.p_full[i & 1], (i >> 1) & 1)) return false;
+      tc::fence_after_sync();
+      issue_pv<D, N>(el, tbase + S::kColO + (uint32_t)o * (2 * N), smem_u32(sm.p[i % S::kPBufs]),
+                     smem_u32(sm.v[s]), !first);
+      tc::commit_elected(el, &sm.v_empty[s]);
+      tc::commit_elected(el, &sm.pv_done);
+      return true;
+    };
+    for (int p = p_begin; ok && p < p_end; ++p) {
+      const DecodePiece pc = tv.pieces[p];
+      if (tv.n[pc.b] <= row0) continue;
+      const RingView ring = ring_view(v, pc.b, pc.plen);
+      const PieceTiles pt(pc, ring);
+      if (pt.n == 0) continue;
+      const int qs = active % NQ;
+      if (!(ok = wait(&sm.q_full[qs], (active / NQ) & 1))) break;
+      if (v.rope && !(ok = wait(&sm.turned, active & 1))) break;
+      const int o = active & 1;
+      for (int j = 0; ok && j < pt.n; ++j, ++it) {
+        const int s = it % NK;
+        if (!(ok = wait(&sm.k_full[s], (it / NK) & 1))) break;
+        tc::fence_after_sync();
+        // overwrites S of tile it - 2, which the softmax had read before its PV
+        issue_qk<D, N>(el, tbase + (uint32_t)(it & 1) * N, smem_u32(sm.q[qs]), smem_u32(sm.k[s]));
+        tc::commit_elected(el, &sm.s_full[it & 1]);
+        tc::commit_elected(el, &sm.k_empty[s]);
+        if (j == pt.n - 1) tc::commit_elected(el, &sm.q_free[qs]);
+        if (j == 1 &&  // the results of the piece before the last are out of this O
+            !(ok = wait(&sm.o_free[o], ((active >> 1) & 1) ^ 1)))
+          break;
+        if (j > 0 && !(ok = pv(it - 1, j == 1, pt.masked(j - 1, ring), o))) break;
+      }
+      if (ok && pt.n == 1) ok = wait(&sm.o_free[o], ((active >> 1) & 1) ^ 1);
+      if (ok && (ok = pv(it - 1, pt.n == 1, pt.masked(pt.n - 1, ring), o)))
+        tc::commit_elected(el, &sm.o_done[o]);
+      ++active;
+    }
+    tc::commit_elected(el, &sm.mma_done);
+    mbar_wait_bounded(&sm.mma_done, 0, v.err, RSWA_DEVERR_TIMEOUT);
+    __syncwarp();
   } else if (warp >= kSide) {
     // ------------------------------------------------------------ side warps
+    constexpr int kSideBar = 1 + S::kGroups;
     const int tid = (int)threadIdx.x - kSide * 32;  // 0..127: a row of a tile, a TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     // element of the output on this lane (64 rows of an MMA take 16 lanes a warp)
@@ -451,7 +465,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
       __syncwarp();
     };
     int it = 0, active = 0;
-    uint32_t scans = 0;
+    uint32_t ask = 0;         // bit s: parity of V slot s's next v_ask
     int last = -1;            // the piece whose results are due
     bool last_mend = false;   // a value that is not finite was taken out of its V
     // The results of piece `last`: final where it is the ring's only one, else a partial.
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           }
         }
       }
-      named_bar_sync(3, 128);  // sm.inv is written
+      named_bar_sync(kSideBar, 128);  // sm.inv is written
       const bool whole = pc.count == 1;
       const int64_t step = whole ? (int64_t)v.H * D : D;  // elements from draft to draft
       __nv_bfloat16 *dst = a.out + (draft0 * v.H + pc.h) * D + elem;
@@ -539,7 +553,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_free[o]);
-      named_bar_sync(3, 128);  // sm.inv is read
+      named_bar_sync(kSideBar, 128);  // sm.inv is read
       last = -1;
     };
     for (int p = p_begin; p < p_end; ++p) {
@@ -555,13 +569,14 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         continue;
       }
       if (v.rope) {
-        wait(&sm.q_full, active & 1);
+        const int qs = active % NQ;
+        wait(&sm.q_full[qs], (active / NQ) & 1);
         if (tid < N && row0 + tid < n)
-          turn_row<D>(sm.q, tid, N * 128, tv.cs + (draft0 + row0 + tid) * (D / 2));
+          turn_row<D>(sm.q[qs], tid, N * 128, tv.cs + (draft0 + row0 + tid) * (D / 2));
         if (pt.drafts) {
-          wait(&sm.k_full[it % NST], (it / NST) & 1);
+          wait(&sm.k_full[it % NK], (it / NK) & 1);
           if (tid < n)
-            turn_row<D>(sm.k[it % NST], tid, kHalfBytes, tv.cs + (draft0 + tid) * (D / 2));
+            turn_row<D>(sm.k[it % NK], tid, kHalfBytes, tv.cs + (draft0 + tid) * (D / 2));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -573,8 +588,13 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           // V's rows that hold no entry become 0, and so do values that are not finite
           const int held = pt.is_drafts(j) ? n : ring.held - pt.slot(j);
           bool bad = false;
-          wait(&sm.v_ask, scans++ & 1u);
-          uint8_t *vt = sm.v[it % NST];
+          const int vs = it % NV;
+          // the load is under way, so v_full's phase before this one is over; and
+          // none comes after it before v_fit
+          wait(&sm.v_ask[vs], (ask >> vs) & 1u);
+          ask ^= 1u << vs;
+          wait(&sm.v_full[vs], (it / NV) & 1);
+          uint8_t *vt = sm.v[vs];
           constexpr int kScan = 8;  // 16-byte chunks of a row looked at together
           for (int c0 = 0; c0 < D / 8; c0 += kScan) {
             uint4 u[kScan];
@@ -596,8 +616,8 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.v_fit);
-          mend |= bar_red_or(3, 128, bad);
+          if (lane == 0) mbar_arrive(&sm.v_fit[vs]);
+          mend |= bar_red_or(kSideBar, 128, bad);
         }
         if (j == 0 && last >= 0) finish();
       }
@@ -612,7 +632,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     const int key = (int)threadIdx.x & 127;     // key row of the tile, and TMEM lane
     const int col0 = group * NC;                // first column of this thread
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const int bar_group = 1 + group;            // hardware barriers: a group's; 3: the side warps'
+    const int bar_group = 1 + group;            // the group's hardware barrier
     const float sl2 = v.scale * kLog2e;
     const uint64_t sl2x2 = tc::f2_pack(sl2, sl2), minus1 = tc::f2_pack(-1.f, -1.f);
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -652,7 +672,8 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         uint32_t sees = 0xffffffffu;  // bit c: draft row0 + col0 + c sees this key
         if (masked) {
           if (pt.is_drafts(j)) {
-            sees = key < n_all ? word_of(tv.below[draft0 + key], (row0 + col0) >> 5) : 0u;
+            sees = key < n_all ? word_of(tv.below[draft0 + key], (row0 + col0) >> 5) >> (col0 & 31)
+                               : 0u;
           } else {
             const int age = slot_age(ring, pt.slot(j) + key);
             const int deepest = age == INT_MIN ? INT_MAX : age == INT_MAX ? -1 : v.W - 1 - age;
