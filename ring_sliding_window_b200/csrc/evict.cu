@@ -34,6 +34,9 @@ __global__ void __launch_bounds__(kFinishThreads)
   const int bh = (int)(blockIdx.x / (unsigned)chunks);
   const int b = bh / v.H, h = bh % v.H;
   const int P = v.plen[b];
+  // No early start for the kernel after this one: the next layer's decode step
+  // would be placed around these CTAs' registers, unevenly (154 us for 122).
+  grid_dependency_wait();
   const int64_t t = v.t[b];
   const int held = P + (int)(t + 1 < v.W ? t + 1 : (int64_t)v.W);
   const int fresh = P + (int)(t % v.W);  // the step's own entry: its score starts over
@@ -58,21 +61,29 @@ __global__ void __launch_bounds__(kFinishThreads)
 }
 
 // ------------------------------------------------------------- selection
-// The K prompt entries with the highest scores of one ring: a radix select
-// over order-preserving 32-bit keys, 8 bits a pass, by a cluster of CTAs that
-// add their histograms through distributed shared memory; then every CTA lists
-// its kept entries in ascending order at its offset of the ring's list.  Reads
-// 4 bytes an entry five times, four of them from L2; latency-bound (about a
-// dozen cluster barriers).
-constexpr int kSelCtas = 8;
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+// The K prompt entries with the highest scores of one ring, by one CTA: a radix
+// select over order-preserving 32-bit keys (11, 11 and 10 bits a pass) finds the
+// K-th largest key and how many of its equals belong in; then the kept entries
+// are listed in ascending order.  Scores are read once, the keys stay in shared
+// memory (beyond kSelCache entries they are read again, from L2), and every loop
+// after the first takes four a thread.
+//
+// Bound by instruction issue (about 40 an entry and lane over five loops) and,
+// for short rings, by the latency of seven short phases.  TODO us for 80 rings of
+// 8,256 entries, TODO us for 40 of 32,640.  Clusters of 2 and 4 CTAs a ring that add
+// their counts through distributed shared memory took longer: what their
+// barriers and remote loads cost is more than the loops.
+constexpr int kSelMaxThreads = 1024;
+constexpr int kSelBins = 2048;
+constexpr int kSelCache = 49152;  // 192 KB
+constexpr int kSelAhead = 8;      // scores of a thread in flight
 
 struct SelectArgs {
   DeviceView src, dst;
   const float *score;
   int n_first, n_last;
   int32_t *kept;
+  int cache;  // keys that the launch's shared memory holds, a multiple of 4
 };
 
 // Larger key = kept first.  NaN ranks below everything, -0 with +0; a
@@ -83,131 +94,190 @@ __device__ __forceinline__ uint32_t score_key(float x, bool guarded) {
   const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+constexpr uint32_t kZeroKey = 0x80000000u;
 
-__global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads)
+// Counts of bins: a thread's runs of one bin (equal scores, protected entries)
+// and its exact zeros, which are many, take one shared atomic each.
+struct BinCounter {
+  uint32_t *hist;
+  uint32_t bin = 0, run = 0, zeros = 0;
+  __device__ __forceinline__ void add(uint32_t b, bool zero) {
+    if (zero) {
+      ++zeros;
+    } else if (b == bin) {
+      ++run;
+    } else {
+      if (run) atomicAdd(&hist[bin], run);
+      bin = b;
+      run = 1;
+    }
+  }
+  __device__ __forceinline__ void finish(uint32_t zero_bin) {
+    if (run) atomicAdd(&hist[bin], run);
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if ((threadIdx.x & 31) == 0 && zeros) atomicAdd(&hist[zero_bin], zeros);
+  }
+};
+
+__global__ void __launch_bounds__(kSelMaxThreads)
     evict_select_kernel(const SelectArgs a) {
-  __shared__ uint32_t hist[2][256];
-  __shared__ uint32_t pick[2];      // bin of the threshold, entries above it
-  __shared__ uint32_t totals[2];    // this CTA's entries above / at the threshold
-  __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
-  const int ring = (int)(blockIdx.x / kSelCtas), rank = (int)(blockIdx.x % kSelCtas);
+  extern __shared__ uint4 sel_smem[];  // [kSelBins] counts, then [a.cache] keys
+  __shared__ uint32_t warp_a[32], warp_b[32];
+  __shared__ uint32_t pick[3];  // bin of the threshold, entries above it, entries in it
+  uint32_t *hist = reinterpret_cast<uint32_t *>(sel_smem), *keys = hist + kSelBins;
+  const int ring = (int)blockIdx.x;
   const int b = ring / a.src.H, h = ring % a.src.H;
   const int P = a.src.plen[b], K = a.dst.plen[b];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (K == 0) return;  // the whole cluster
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int64_t row0 = (int64_t)a.src.H * a.src.slot_base[b] + (int64_t)h * (P + a.src.W);
+  const int64_t list0 = (int64_t)a.src.H * a.dst.tok_base[b] + (int64_t)h * K;
   const float *score = a.score + row0;
-  const int seg = (P + kSelCtas - 1) / kSelCtas;
-  const int s0 = min(P, rank * seg), s1 = min(P, s0 + seg);
-  auto key_at = [&](int s) {
-    return score_key(score[s], s < a.n_first || s >= P - a.n_last);
+  grid_dependency_wait();
+  allow_dependents();
+  if (K == 0) return;
+  if (K == P) {
+    for (int s = tid; s < P; s += nt) a.kept[list0 + s] = s;
+    return;
+  }
+  auto to_key = [&](float x, int s) {
+    return score_key(x, s < a.n_first || s >= P - a.n_last);
+  };
+  // keys of entries 4 i .. 4 i + 3 (behind the last entry: anything)
+  const int quads = (P + 3) / 4;
+  auto key4 = [&](int i) {
+    if (4 * i < a.cache) return *reinterpret_cast<const uint4 *>(keys + 4 * i);
+    uint32_t k[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      k[c] = 4 * i + c < P ? to_key(score[4 * i + c], 4 * i + c) : 0u;
+    return make_uint4(k[0], k[1], k[2], k[3]);
   };
 
-  uint32_t prefix = 0;       // the threshold's leading bits so far
-  uint32_t left = (uint32_t)K;  // entries still to take among keys with that prefix
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    uint32_t *hs = hist[pass & 1];
-    for (int i = tid; i < 256; i += kSelThreads) hs[i] = 0;
+  uint32_t prefix = 0;           // the threshold's leading bits so far
+  uint32_t left = (uint32_t)K;   // entries still to take among keys with that prefix
+  int shift = 32;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass < 2 ? 11 : 10;
+    const uint32_t bins = 1u << bits;
+    const int above = shift;     // bits of a key above this pass's lie at this shift
+    shift -= bits;
+    for (int i = tid; i < (int)bins; i += nt) hist[i] = 0;
     __syncthreads();
-    for (int s = s0 + tid; s < s0 + (s1 - s0 + 31) / 32 * 32; s += kSelThreads) {
-      uint32_t bin = 256;  // none
-      if (s < s1) {
-        const uint32_t k = key_at(s);
-        if (pass == 0 || (k >> (shift + 8)) == prefix) bin = (k >> shift) & 255u;
+    BinCounter counter{hist};
+    if (pass == 0) {
+      for (int s0 = tid; s0 < P; s0 += kSelAhead * nt) {
+        float x[kSelAhead];
+#pragma unroll
+        for (int u = 0; u < kSelAhead; ++u) x[u] = s0 + u * nt < P ? score[s0 + u * nt] : 0.f;
+#pragma unroll
+        for (int u = 0; u < kSelAhead; ++u) {
+          const int s = s0 + u * nt;
+          if (s < P) {
+            const uint32_t k = to_key(x[u], s);
+            if (s < a.cache) keys[s] = k;
+            counter.add(k >> shift, k == kZeroKey);
+          }
+        }
       }
-      // many entries share a bin (ties at zero, one exponent): the warp's first
-      // lane adds for all lanes with its bin, the others one by one
-      const uint32_t bin0 = __shfl_sync(0xffffffffu, bin, 0);
-      const uint32_t same = __ballot_sync(0xffffffffu, bin == bin0);
-      if (lane == 0) {
-        if (bin0 < 256) atomicAdd(&hs[bin0], (uint32_t)__popc(same));
-      } else if (bin != bin0 && bin < 256) {
-        atomicAdd(&hs[bin], 1u);
+    } else {
+#pragma unroll 2
+      for (int i = tid; i < quads; i += nt) {
+        const uint4 q = key4(i);
+        const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if ((k[c] >> above) == prefix && 4 * i + c < P)
+            counter.add((k[c] >> shift) & (bins - 1), k[c] == kZeroKey);
       }
     }
-    cluster_arrive_release();
-    cluster_wait_acquire();
-    // bins from the highest down: thread i holds bin 255 - i of the whole ring
-    uint32_t mine = 0, run = 0;
-    if (tid < 256) {
-      for (int r = 0; r < kSelCtas; ++r) mine += ld_cluster_u32(map_to_rank(&hs[255 - tid], r));
-      run = mine;
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t up = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += up;
-      }
-      if (lane == 31) warp_gt[warp] = run;
+    __syncwarp();
+    counter.finish((kZeroKey >> shift) & (bins - 1));
+    __syncthreads();
+    // bins from the highest down, bins / nt of them a thread
+    const int per = (int)bins / nt;
+    const int top = (int)bins - 1 - tid * per;
+    uint32_t mine = 0;
+    for (int i = 0; i < per; ++i) mine += hist[top - i];
+    uint32_t run = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
+    }
+    if (lane == 31) warp_a[warp] = run;
+    __syncthreads();
+    run += __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0u);
+    uint32_t before = run - mine;
+    if (before < left && run >= left) {
+      int i = 0;
+      for (; before + hist[top - i] < left; ++i) before += hist[top - i];
+      pick[0] = (uint32_t)(top - i);
+      pick[1] = before;
+      pick[2] = hist[top - i];
     }
     __syncthreads();
-    if (tid < 256) {
-      for (int w = 0; w < warp; ++w) run += warp_gt[w];
-      if (run >= left && run - mine < left) {
-        pick[0] = 255u - (uint32_t)tid;
-        pick[1] = run - mine;
-      }
-    }
-    __syncthreads();
-    prefix = (prefix << 8) | pick[0];
+    prefix = (prefix << bits) | pick[0];
     left -= pick[1];
-    __syncthreads();  // pick and warp_gt are read
+    if (pick[2] == left) {  // the whole bin is kept: no need to look further into it
+      left = 0xffffffffu;
+      break;
+    }
   }
-  // kept: every key above `prefix`, and the first `left` of those equal to it
-  if (tid < 2) totals[tid] = 0;
+  // kept: every key above the threshold, and the first `left` of those equal to
+  // it; a warp takes a stretch of the ring, a lane four neighbours of every 128
+  const uint32_t thr = prefix << shift;
+  const int span = ((quads + 31) / 32 + warps - 1) / warps * 32;  // quads of a warp
+  const int i0 = warp * span, i1 = min((quads + 31) / 32 * 32, i0 + span);
+  uint32_t gt = 0, eq = 0;
+#pragma unroll 2
+  for (int i = i0 + lane; i < i1; i += 32) {
+    if (i >= quads) break;
+    const uint4 q = key4(i);
+    const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      gt += 4 * i + c < P && k[c] > thr ? 1u : 0u;
+      eq += 4 * i + c < P && k[c] == thr ? 1u : 0u;
+    }
+  }
+  __syncwarp();
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  __syncthreads();  // warp_a is read
+  if (lane == 0) {
+    warp_a[warp] = gt;
+    warp_b[warp] = eq;
+  }
   __syncthreads();
-  {
-    uint32_t gt = 0, eq = 0;
-    for (int s = s0 + tid; s < s1; s += kSelThreads) {
-      const uint32_t k = key_at(s);
-      gt += k > prefix;
-      eq += k == prefix;
+  // entries above and at the threshold before this warp's next 128
+  uint32_t g = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0u);
+  uint32_t e = __reduce_add_sync(0xffffffffu, lane < warp ? warp_b[lane] : 0u);
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint4 q = i < quads ? key4(i) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+    uint32_t mine = 0;  // above the threshold, and at it in the upper half
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (4 * i + c < P) mine += k[c] > thr ? 1u : k[c] == thr ? 0x10000u : 0u;
+    uint32_t run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
     }
-    for (int o = 16; o > 0; o >>= 1) {
-      gt += __shfl_xor_sync(0xffffffffu, gt, o);
-      eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    const uint32_t all = __shfl_sync(0xffffffffu, run, 31);
+    uint32_t my_g = g + ((run - mine) & 0xffffu), my_e = e + ((run - mine) >> 16);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (4 * i + c >= P || k[c] < thr) continue;
+      const bool is_gt = k[c] > thr;
+      if (is_gt || my_e < left) a.kept[list0 + my_g + min(my_e, left)] = 4 * i + c;
+      my_g += is_gt ? 1u : 0u;
+      my_e += is_gt ? 0u : 1u;
     }
-    if (lane == 0) {
-      atomicAdd(&totals[0], gt);
-      atomicAdd(&totals[1], eq);
-    }
+    g += all & 0xffffu;
+    e += all >> 16;
   }
-  cluster_arrive_release();
-  cluster_wait_acquire();
-  uint32_t n_gt = 0, n_eq = 0;  // in the segments before the current 512 entries
-  for (int r = 0; r < rank; ++r) {
-    n_gt += ld_cluster_u32(map_to_rank(&totals[0], r));
-    n_eq += ld_cluster_u32(map_to_rank(&totals[1], r));
-  }
-  int64_t list0 = 0;  // this ring's list: H sum_{b' < b} P'_b' + h P'_b
-  list0 = (int64_t)a.src.H * a.dst.tok_base[b] + (int64_t)h * K;
-  for (int base = s0; base < s1; base += kSelThreads) {
-    const int s = base + tid;
-    const uint32_t k = s < s1 ? key_at(s) : 0u;
-    const bool gt = s < s1 && k > prefix, eq = s < s1 && k == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      warp_gt[warp] = (uint32_t)__popc(bg);
-      warp_eq[warp] = (uint32_t)__popc(be);
-    }
-    __syncthreads();
-    uint32_t g = n_gt, e = n_eq;
-    for (int w = 0; w < kSelWarps; ++w) {
-      if (w < warp) {
-        g += warp_gt[w];
-        e += warp_eq[w];
-      }
-      n_gt += warp_gt[w];
-      n_eq += warp_eq[w];
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    g += (uint32_t)__popc(bg & below);
-    e += (uint32_t)__popc(be & below);
-    if (gt || (eq && e < left)) a.kept[list0 + g + (e < left ? e : left)] = s;
-    __syncthreads();
-  }
-  // no CTA leaves while another may still read its shared memory
-  cluster_arrive_release();
-  cluster_wait_acquire();
 }
 
 // ------------------------------------------------------------------ move
@@ -236,6 +306,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
   const int ring = (int)(blockIdx.x / (unsigned)a.groups);
   const int b = ring / a.src.H, h = ring % a.src.H;
   const int P = a.src.plen[b], K = a.dst.plen[b], W = a.src.W;
+  grid_dependency_wait();  // (and no early start for the next kernel: this one writes prompt rows)
   const int64_t t = a.src.t[b];
   const int n = K + (int)(t < W ? t : (int64_t)W);
   const int64_t src0 = (int64_t)a.src.H * a.src.slot_base[b] + (int64_t)h * (P + W);
@@ -306,9 +377,8 @@ bool share_memory(const std::vector<std::pair<uintptr_t, uintptr_t>> &a,
 cudaError_t launch_score_finish(const DeviceView &v, const float *raw, const float *score_in,
                                 float *score_out, cudaStream_t s) {
   const int chunks = (v.max_plen + v.W + kFinishThreads * kFinishPer - 1) / (kFinishThreads * kFinishPer);
-  score_finish_kernel<<<(unsigned)(v.B * v.H) * (unsigned)chunks, kFinishThreads, 0, s>>>(
-      v, raw, score_in, score_out, chunks);
-  return cudaGetLastError();
+  return launch_overlapped(score_finish_kernel, dim3((unsigned)(v.B * v.H) * (unsigned)chunks),
+                           dim3(kFinishThreads), 0, s, v, raw, score_in, score_out, chunks);
 }
 
 }  // namespace rswa
@@ -379,9 +449,22 @@ rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, co
   }
   const cudaStream_t st = (cudaStream_t)stream;
   const unsigned rings = (unsigned)(a.batch * a.num_heads);
-  const SelectArgs sel{src->dv, dst->dv, score, n_first, n_last, kept};
-  evict_select_kernel<<<rings * kSelCtas, kSelThreads, 0, st>>>(sel);
-  cudaError_t e = cudaGetLastError();
+  const int max_p = src->dv.max_plen;
+  const SelectArgs sel{src->dv, dst->dv, score, n_first, n_last, kept,
+                       std::min((max_p + 3) / 4 * 4, kSelCache)};
+  static bool attr_set[64] = {};  // per device
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    const cudaError_t err =
+        cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (kSelBins + kSelCache) * (int)sizeof(uint32_t));
+    if (err != cudaSuccess) return from_cuda(err);
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  // about four entries a thread, in the longest ring, until a CTA is full
+  int threads = 128;
+  while (threads < kSelMaxThreads && threads * 4 < max_p) threads *= 2;
+  cudaError_t e = launch_overlapped(evict_select_kernel, dim3(rings), dim3((unsigned)threads),
+                                    (size_t)(kSelBins + sel.cache) * sizeof(uint32_t), st, sel);
   if (e != cudaSuccess) return from_cuda(e);
   MoveArgs mv;
   mv.src = src->dv;
@@ -396,13 +479,10 @@ rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, co
   constexpr int kPerCta = kMoveThreads / 32 * kMoveRows;
   mv.groups = (dst->dv.max_plen + a.window + kPerCta - 1) / kPerCta;
   const unsigned grid = rings * (unsigned)mv.groups;
-  if (row_bytes == 128)
-    evict_move_kernel<128><<<grid, kMoveThreads, 0, st>>>(mv);
-  else if (row_bytes == 256)
-    evict_move_kernel<256><<<grid, kMoveThreads, 0, st>>>(mv);
-  else
-    evict_move_kernel<512><<<grid, kMoveThreads, 0, st>>>(mv);
-  e = cudaGetLastError();
+  auto *move = row_bytes == 128   ? evict_move_kernel<128>
+               : row_bytes == 256 ? evict_move_kernel<256>
+                                  : evict_move_kernel<512>;
+  e = launch_overlapped(move, dim3(grid), dim3(kMoveThreads), 0, st, mv);
   if (e != cudaSuccess) return from_cuda(e);
   dst->dv.rope = src->dv.rope;
   dst->dv.rope_theta = src->dv.rope_theta;
