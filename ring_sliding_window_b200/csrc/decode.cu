@@ -84,6 +84,7 @@ struct __align__(128) DecodeSmem {
   // leader's copy through distributed shared memory
   float cl_o[kCluster ? kMaxCluster : 1][D];
   float2 cl_ml[kCluster ? kMaxCluster : 1];
+  float2 ring_ml;  // scored step: the ring's (m, l), from the leader
   uint64_t full[NST];
   uint64_t empty[NST];
 };
@@ -163,6 +164,8 @@ struct DecodeArgs {
   void *kc, *vc;
   void *out;
   float *raw;  // scored step: every attended entry's score in log2 units, by cache row
+  const float *score_in;  // scored step of the cluster form, which also adds the
+  float *score_out;       // weights up (the other form leaves that to a second kernel)
 };
 
 
@@ -533,6 +536,27 @@ __global__ void __launch_bounds__(DecodeShape<T, D>::kThreads)
           acc = (a4[0] + a4[1]) + (a4[2] + a4[3]);
         }
         store_result<T, D, kScored>(v, a, pc.b * v.H + pc.h, tid, Mg, Lg, acc);
+        if (kScored && tid < C) {
+          const uint32_t dst = map_to_rank(&sm.ring_ml, (uint32_t)tid);
+          st_cluster_f32x2(dst, Mg, Lg);
+        }
+      }
+      if constexpr (kScored) {
+        // score_out = score_in + 2^(s - m) / l over this CTA's entries; the step's
+        // own entry starts over, and entries in front of the window keep theirs
+        __syncwarp();
+        cluster_arrive_release();
+        cluster_wait_acquire();
+        const float2 ml = sm.ring_ml;
+        const float inv = 1.f / ml.y;
+        const int64_t t = v.t[pc.b];
+        const int fresh = pc.plen + (int)(t % v.W);
+        for (int s = kr.kb + tid; s < kr.ke; s += 128) {
+          const float before = s == fresh ? 0.f : a.score_in[pc.row0 + s];
+          a.score_out[pc.row0 + s] = fmaf(exp2f(a.raw[pc.row0 + s] - ml.x), inv, before);
+        }
+        if (v.swa && rank == 0)
+          for (int s = tid; s < kr.kb; s += 128) a.score_out[pc.row0 + s] = a.score_in[pc.row0 + s];
       }
       continue;  // a cluster CTA has exactly one piece
     }
@@ -615,7 +639,7 @@ cudaError_t set_smem_attr() {
 template <typename T, int D, bool kCluster, bool kScored>
 cudaError_t launch_decode_t(const DeviceView &v, const void *q, const void *k_new,
                             const void *v_new, void *kc, void *vc, void *out, cudaStream_t s,
-                            bool pdl, float *raw) {
+                            bool pdl, const ScoredStep &sc) {
   using S = DecodeShape<T, D>;
   // per instantiation and device; the plain forms' are also set when the state is built
   static bool attr_set[64] = {};
@@ -625,7 +649,7 @@ cudaError_t launch_decode_t(const DeviceView &v, const void *q, const void *k_ne
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  DecodeArgs a{v, q, k_new, v_new, kc, vc, out, raw};
+  DecodeArgs a{v, q, k_new, v_new, kc, vc, out, sc.raw, sc.in, sc.out};
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(kCluster ? v.B * v.H * v.cluster_size : v.decode_grid);
   lc.blockDim = dim3(S::kThreads);
@@ -650,14 +674,14 @@ cudaError_t launch_decode_t(const DeviceView &v, const void *q, const void *k_ne
 template <typename T, int D>
 cudaError_t launch_decode_d(const DeviceView &v, const void *q, const void *k_new,
                             const void *v_new, void *kc, void *vc, void *out, cudaStream_t s,
-                            bool pdl, float *raw) {
-  if (raw)
+                            bool pdl, const ScoredStep &sc) {
+  if (sc.raw)
     return v.cluster_size > 0
-               ? launch_decode_t<T, D, true, true>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw)
-               : launch_decode_t<T, D, false, true>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
+               ? launch_decode_t<T, D, true, true>(v, q, k_new, v_new, kc, vc, out, s, pdl, sc)
+               : launch_decode_t<T, D, false, true>(v, q, k_new, v_new, kc, vc, out, s, pdl, sc);
   return v.cluster_size > 0
-             ? launch_decode_t<T, D, true, false>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw)
-             : launch_decode_t<T, D, false, false>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
+             ? launch_decode_t<T, D, true, false>(v, q, k_new, v_new, kc, vc, out, s, pdl, sc)
+             : launch_decode_t<T, D, false, false>(v, q, k_new, v_new, kc, vc, out, s, pdl, sc);
 }
 
 template <typename T, int D>
@@ -700,14 +724,14 @@ int max_clusters_t(int cluster) {
 
 cudaError_t launch_decode(const DeviceView &v, const void *q, const void *k_new,
                           const void *v_new, void *kc, void *vc, void *out, cudaStream_t s,
-                          bool pdl, float *raw) {
+                          bool pdl, const ScoredStep &sc) {
   if (v.dtype == RSWA_BF16) {
     if (v.D == 128)
-      return launch_decode_d<__nv_bfloat16, 128>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
-    return launch_decode_d<__nv_bfloat16, 64>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
+      return launch_decode_d<__nv_bfloat16, 128>(v, q, k_new, v_new, kc, vc, out, s, pdl, sc);
+    return launch_decode_d<__nv_bfloat16, 64>(v, q, k_new, v_new, kc, vc, out, s, pdl, sc);
   }
-  if (v.D == 128) return launch_decode_d<float, 128>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
-  return launch_decode_d<float, 64>(v, q, k_new, v_new, kc, vc, out, s, pdl, raw);
+  if (v.D == 128) return launch_decode_d<float, 128>(v, q, k_new, v_new, kc, vc, out, s, pdl, sc);
+  return launch_decode_d<float, 64>(v, q, k_new, v_new, kc, vc, out, s, pdl, sc);
 }
 
 // Log-sum-exp merge of `shares` partials (m, l, o) per ring: one CTA per ring,

@@ -403,8 +403,10 @@ rswa_status rswa_decode_step_scored(rswa_state *s, int32_t layer, const void *q,
   if (current_device() != s->device) return RSWA_EINVAL;
   const cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = launch_decode(s->dv, q, k_new, v_new, s->k_cache[(size_t)layer],
-                                s->v_cache[(size_t)layer], out, st, true, scratch);
-  if (e == cudaSuccess) e = launch_score_finish(s->dv, scratch, score_in, score_out, st);
+                                s->v_cache[(size_t)layer], out, st, true,
+                                {scratch, score_in, score_out});
+  if (e == cudaSuccess && s->dv.cluster_size == 0)
+    e = launch_score_finish(s->dv, scratch, score_in, score_out, st);
   return from_cuda(e);
 }
 

@@ -149,11 +149,18 @@ namespace rswa {
 // Launchers (return cudaGetLastError() of their launch).
 // pdl: launch with programmatic stream serialization (the kernel waits for
 // the previous kernel's completion before touching any produced data).
-// raw: non-null makes it a scored step: every attended entry's score (log2
-// units) goes to raw[cache row] and every ring's (m, l) to v.ring_ml.
+// A scored step (raw is not null): every attended entry's score (log2 units) goes
+// to raw[cache row] and every ring's (m, l) to v.ring_ml.  With clusters
+// (v.cluster_size > 0) the step also writes out = in + weights; else
+// launch_score_finish has to follow.
+struct ScoredStep {
+  float *raw = nullptr;
+  const float *in = nullptr;
+  float *out = nullptr;
+};
 cudaError_t launch_decode(const DeviceView &v, const void *q, const void *k_new,
                           const void *v_new, void *kc, void *vc, void *out, cudaStream_t s,
-                          bool pdl, float *raw = nullptr);
+                          bool pdl, const ScoredStep &sc = {});
 cudaError_t launch_advance(const DeviceView &v, cudaStream_t s);
 cudaError_t launch_combine(const float2 *ml, const float *o, int shares, int64_t rings, int D,
                            int dtype, void *out, cudaStream_t s);
