@@ -34,7 +34,7 @@ struct SimtSmem {
   float q[kRows][D + 4];
   float k[kKeys][D + 4];
   float v[kKeys][D + 4];
-  float p[kRows][kKeys + 1];
+  float p[kRows][kKeys + 4];
   float alpha[kRows];
   int limit[kRows];     // W - 1 - depth of the row
   uint4 above[kRows];
@@ -65,9 +65,11 @@ __device__ __forceinline__ void load_rotated(const float *src, float *dst, int c
       x = a[e] * r.x - b[e] * r.y;
       y = b[e] * r.x + a[e] * r.y;
     }
-    dst[c * N + e] = x;
-    dst[c * N + e + D / 2] = y;
+    a[e] = x;
+    b[e] = y;
   }
+  *reinterpret_cast<float4 *>(dst + c * N) = make_float4(a[0], a[1], a[2], a[3]);
+  *reinterpret_cast<float4 *>(dst + c * N + D / 2) = make_float4(b[0], b[1], b[2], b[3]);
 }
 
 template <int D, int kRows>
@@ -211,21 +213,29 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int c = 0; c < kCT * 4; ++c) acc[i][c] *= corr;
       }
-      for (int j = 0; j < nk; ++j) {
-        float4 vv[kCT];
+#pragma unroll 2
+      for (int j0 = 0; j0 < nk; j0 += 4) {  // (rows of V behind the last entry have w < 0)
+        float4 w4[kRT];
 #pragma unroll
-        for (int c = 0; c < kCT; ++c)
-          vv[c] = *reinterpret_cast<const float4 *>(&sm.v[j][tx * 4 + 64 * c]);
+        for (int i = 0; i < kRT; ++i)
+          w4[i] = *reinterpret_cast<const float4 *>(&sm.p[ty + 16 * i][j0]);
 #pragma unroll
-        for (int i = 0; i < kRT; ++i) {
-          const float w = sm.p[ty + 16 * i][j];
-          if (w >= 0.f) {  // an unseen entry's value never enters, whatever it holds
+        for (int u = 0; u < 4; ++u) {
+          float4 vv[kCT];
 #pragma unroll
-            for (int c = 0; c < kCT; ++c) {
-              acc[i][4 * c] = fmaf(w, vv[c].x, acc[i][4 * c]);
-              acc[i][4 * c + 1] = fmaf(w, vv[c].y, acc[i][4 * c + 1]);
-              acc[i][4 * c + 2] = fmaf(w, vv[c].z, acc[i][4 * c + 2]);
-              acc[i][4 * c + 3] = fmaf(w, vv[c].w, acc[i][4 * c + 3]);
+          for (int c = 0; c < kCT; ++c)
+            vv[c] = *reinterpret_cast<const float4 *>(&sm.v[j0 + u][tx * 4 + 64 * c]);
+#pragma unroll
+          for (int i = 0; i < kRT; ++i) {
+            const float w = u == 0 ? w4[i].x : u == 1 ? w4[i].y : u == 2 ? w4[i].z : w4[i].w;
+            if (w >= 0.f || w != w) {  // an unseen entry's value never enters, whatever it holds
+#pragma unroll
+              for (int c = 0; c < kCT; ++c) {
+                acc[i][4 * c] = fmaf(w, vv[c].x, acc[i][4 * c]);
+                acc[i][4 * c + 1] = fmaf(w, vv[c].y, acc[i][4 * c + 1]);
+                acc[i][4 * c + 2] = fmaf(w, vv[c].z, acc[i][4 * c + 2]);
+                acc[i][4 * c + 3] = fmaf(w, vv[c].w, acc[i][4 * c + 3]);
+              }
             }
           }
         }
