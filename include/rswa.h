@@ -423,13 +423,15 @@ rswa_status rswa_tree_destroy(rswa_tree *tree);
  * as they were, its commit takes nothing, and RSWA_DEVERR_BAD_TREE or
  * RSWA_DEVERR_BAD_LENGTH goes into the state's device error word.  With RoPE
  * on the nodes' positions are worked out from the ring counters here: call it
- * after the previous step's rswa_tree_advance. */
+ * after the previous step's rswa_tree_advance, and again after a change of the
+ * RoPE setting. */
 rswa_status rswa_tree_set(rswa_tree *tree, const int32_t *parent, const int32_t *n_draft,
                           void *stream);
 
 /* Attention of one layer's drafted tokens.
- *  q, k_draft, v_draft, out : device [B][T][H][d], 16-byte aligned; rows
- *            i >= n_draft[b] are neither read nor written.
+ *  q, k_draft, v_draft, out : device [B][T][H][d], 16-byte aligned, out none of
+ *            the others; rows i >= n_draft[b] of out are not written, and what
+ *            the others hold there does not matter.
  * Values of entries that a node does not attend to never reach its output,
  * infinities and NaN included.  RSWA_EINVAL for a bad layer or pointer,
  * RSWA_ESTATE as rswa_decode_step. */

@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(DecodeShape<T, D>::kThreads)
 
   // Prompt rows (slots < P_b) are written only by the prefill's cache fill
   // or by the caller, never by a kernel that lets its dependents start early
-  // (only this kernel and the ring advance do, and neither writes a prompt
-  // row).  So the first stages of this CTA's first piece that lie wholly in
+  // (this kernel, the ring advance, the draft-tree kernels and the selection of
+  // an eviction do, and none of them writes a prompt row).  So the first stages of this CTA's first piece that lie wholly in
   // the prompt can be requested before the grid-dependency wait; this
   // overlaps their memory latency with the tail of the previous layer.
   int pre_stages = 0;

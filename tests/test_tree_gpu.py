@@ -202,10 +202,11 @@ def test_values_that_every_draft_sees_reach_it(dtype, d, bad):
     assert torch.equal(out[..., others], clean[..., others])
 
 
-def test_dropped_copies_end_with_a_timeout_status():
+@pytest.mark.parametrize("d,T", [(128, 4), (64, 20), (128, 40), (64, 100)])
+def test_dropped_copies_end_with_a_timeout_status(d, T):
     """With the kernel's cache copies dropped every wait runs out, and says so."""
     rswa = _rswa()
-    c = Case(BF, 128, 1, 8, (200,), (3,), 40)
+    c = Case(BF, d, 1, 8, (200, 30), (3, 9), T)
     c.run()
     q, k, v = c.q.cuda(), c.k.cuda(), c.v.cuda()
     out = torch.empty_like(q)
@@ -309,6 +310,56 @@ def test_standard_window_matches_the_definition(dtype, d):
     c = Case(dtype, d, 2, 70, (300, 40, 71), (20, 90, 0), 13)
     c.st.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)
     c.check(c.run(), swa=True)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+@pytest.mark.parametrize("swa", [False, True])
+def test_wide_trees(dtype, d, swa):
+    """More drafts than one group of rows takes, in some sequences only: counts around the
+    group's edge, a branch that crosses it, and bad values in the first group's rows."""
+    rswa = _rswa()
+    T, n = 100, (100, 65, 64, 1, 0)
+    rng = np.random.default_rng(12)
+    parents = [ref.random_parents(rng, T, reach=40) for _ in n]
+    c = Case(dtype, d, 2, 40, (300, 20, 77, 0, 50), (50, 3, 200, 39, 1), T, n=n, parents=parents)
+    if swa:
+        c.st.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)
+    rows = (0, 1, 31, 32, 62, 63, 64, 65, 98, 99)
+    clean = c.run()
+    c.check(clean, swa=swa, rows=rows)
+    c.v[0, 10, :, 3] = float("nan")
+    out = c.run()
+    sees = [i for i in range(T) if 10 in ref.path_of(parents[0], i)[-40:]]
+    blind = [i for i in range(T) if i not in sees]
+    assert torch.equal(out[0, blind], clean[0, blind]) and torch.equal(out[1:], clean[1:])
+    assert bool(out[0, sees, :, 3].isnan().all())
+    others = [e for e in range(d) if e != 3]
+    assert torch.equal(out[0, sees][..., others], clean[0, sees][..., others])
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("rope", [1, 2])
+def test_wide_trees_turn_with_rope(dtype, d, rope):
+    """Every node of a 100-node tree under RoPE gives what a tree of its path alone gives."""
+    T, plens, t = 100, (140, 9), (20, 3)
+    c = Case(dtype, d, 2, 16, plens, t, T, n=(T, 70))
+    c.st.set_rope(rope)
+    out = c.run()
+    for b, i in ((0, 99), (0, 64), (0, 63), (1, 69), (1, 5)):
+        path = ref.path_of(c.parents[b], i)
+        m = len(path)
+        one = c.st.tree(m)
+        q, k, v = (torch.zeros(2, m, 2, d, dtype=dtype) for _ in range(3))
+        for x, y in ((q, c.q), (k, c.k), (v, c.v)):
+            x[b] = y[b, path]
+        n = [m if x == b else 0 for x in range(2)]
+        got = torch.zeros(2, m, 2, d, dtype=dtype, device="cuda")
+        one.set(None, _ints(n))
+        one.attention(0, q.cuda(), k.cuda(), v.cuda(), got)
+        # the same sums in another order, and another subtracted maximum
+        tol = 2e-2 if dtype == BF else 1e-5
+        assert float((got[b, -1].cpu().double() - out[b, i].double()).abs().max()) <= tol
+    assert c.st.check() == 0
 
 
 @pytest.mark.parametrize("dtype,d", KINDS)
