@@ -4,21 +4,28 @@
 // For draft i of a sequence, over the entries j that it may see (the cache's
 // prompt and ring slots, and the drafts above it in the tree),
 //   o_i = sum_j 2^(s_ij - m_i) v_j / sum_j 2^(s_ij - m_i),
-//   s_ij = scale log2(e) q_i.k_j,  m_i = max_j s_ij,
-// in one pass over K and V with the running (m, l, o) of the online softmax.
+//   s_ij = scale log2(e) q_i.k_j,
+// in one pass over K and V.  The keys of all rings are cut into one range of
+// tiles per CTA (the work plan of the tree); a ring in several pieces leaves
+// partials that tree_combine_kernel merges.
 //
-// The keys of all rings are cut into one range of tiles per CTA (the work
-// plan of the tree), so one K/V byte is read once for all the drafts of a row
-// group; a ring in several pieces leaves partials that tree_combine_kernel
-// merges.  A tile is 64 keys: 256 threads form a 16 x 16 grid, each with
-// kRows / 16 query rows x 4 keys of the scores, then the same rows x D / 16
-// output columns.  Groups of 16 rows (fewer than 17 drafts) or 64.  Bound by
-// FP32 FMA issue once a row group is full.
+// Up to 16 drafts: tree_rows_kernel.  A warp takes four drafts, their queries
+// and outputs in registers, and four keys at a time, 8 lanes a key; a producer
+// warp streams K and V rows into shared memory by bulk copies.  Every 16 bytes
+// that leave shared memory meet four drafts, in packed FP32 pairs, so HBM stays
+// the bound up to 8 drafts and FMA issue is close to it at 16.
+//
+// More: tree_simt_kernel, row groups of 64.  A tile is 64 keys: 256 threads form
+// a 16 x 16 grid, each with 4 query rows x 4 keys of the scores, then the same
+// rows x D / 16 output columns.  Bound by FP32 FMA issue and the barriers between
+// its phases.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tcgen05.cuh"
 #include "tree.cuh"
 
 namespace rswa {
@@ -27,6 +34,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKeys = kTreeSimtTile;
 constexpr int kThreads = 256;
+constexpr int kRowsMax = 16;      // drafts that tree_rows_kernel takes
 constexpr float kMasked = -1.f;  // marks an unseen pair where a weight (>= 0) would stand
 
 template <int D, int kRows>
@@ -273,28 +281,335 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <int D, int kRows>
-cudaError_t set_attr() {
-  return cudaFuncSetAttribute(tree_simt_kernel<D, kRows>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sizeof(SimtSmem<D, kRows>));
+// ------------------------------------------------------- up to 16 drafts
+constexpr int kRowWarps = 8;            // consumer warps
+constexpr int kPerWarp = 4;             // drafts of a warp
+constexpr float kGrowth = 8.f;          // m moves past a score 2^8 above it
+
+template <int D>
+struct __align__(128) RowsSmem {
+  static constexpr int kRows = 4096 / D;  // keys of a stage: 16 KB of K, and of V
+  static constexpr int kStages = 5;
+  float k[kStages][kRows * D], v[kStages][kRows * D];
+  float red_o[kRowWarps][kPerWarp][D];
+  float red_m[kRowWarps][kPerWarp], red_l[kRowWarps][kPerWarp];
+  uint64_t full[kStages], empty[kStages];
+};
+
+// G groups of four drafts, 8 / G warps each.
+template <int D, int G>
+__global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
+    tree_rows_kernel(const TreeSimtArgs a) {
+  using Smem = RowsSmem<D>;
+  constexpr int NST = Smem::kStages, kRows = Smem::kRows;
+  constexpr int kWarps = kRowWarps / G;   // of a group
+  constexpr int NP = D / 16;              // pairs of a row's elements on a lane
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+  const DeviceView &v = a.v;
+  const TreeView &tv = a.tv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int p_begin = tv.cta_piece[blockIdx.x], p_end = tv.cta_piece[blockIdx.x + 1];
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], kRowWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  allow_dependents();
+  // a piece's cache slots [k0, k1)
+  auto slots = [&](const DecodePiece &pc, const RingView &ring, int &k0, int &k1) {
+    k0 = max(max(0, pc.key_begin - 1) * kKeys, ring.lo);
+    k1 = max(k0, min((pc.key_end - 1) * kKeys, ring.held));
+  };
+
+  if (warp == kRowWarps) {
+    // -------------------------------------------------------------- producer
+    // test-only fault injection: no copies at all, so every wait runs out
+    if (lane != 0 || (*v.fault & RSWA_FAULT_DROP_DECODE_COPIES) != 0) return;
+    int it = 0;
+    bool ok = true;
+    for (int p = p_begin; ok && p < p_end; ++p) {
+      const DecodePiece pc = tv.pieces[p];
+      if (tv.n[pc.b] == 0) continue;
+      const RingView ring = ring_view(v, pc.b, pc.plen);
+      int k0, k1;
+      slots(pc, ring, k0, k1);
+      for (; k0 < k1; k0 += kRows, ++it) {
+        const int s = it % NST;
+        if (!(ok = mbar_wait_bounded(&sm.empty[s], ((it / NST) & 1) ^ 1, v.err, RSWA_DEVERR_TIMEOUT)))
+          break;
+        const uint32_t bytes = (uint32_t)min(kRows, k1 - k0) * (uint32_t)(D * sizeof(float));
+        mbar_arrive_expect_tx(&sm.full[s], 2 * bytes);
+        bulk_g2s(sm.k[s], a.kc + (pc.row0 + k0) * D, bytes, &sm.full[s]);
+        bulk_g2s(sm.v[s], a.vc + (pc.row0 + k0) * D, bytes, &sm.full[s]);
+      }
+    }
+    // every copy issued has landed before the CTA may exit (bounded)
+    for (int s = 0; s < NST && s < it; ++s)
+      mbar_wait_bounded(&sm.full[s], ((it - 1 - s) / NST) & 1, v.err, RSWA_DEVERR_TIMEOUT);
+    return;
+  }
+
+  // --------------------------------------------------------------- consumers
+  const int li = lane & 7, lg = lane >> 3;       // lane of a key, key of four
+  const int group = warp / kWarps, wg = warp % kWarps;
+  const float qs = v.scale * kLog2e;
+  int it = 0;
+  bool dead = false;
+  for (int p = p_begin; p < p_end; ++p) {
+    const DecodePiece pc = tv.pieces[p];
+    const int n = tv.n[pc.b];
+    if (n == 0) continue;
+    const RingView ring = ring_view(v, pc.b, pc.plen);
+    const int64_t draft0 = (int64_t)pc.b * tv.T;
+    // a row's chunks li, li + 8, ... (16 bytes each) as packed pairs, turned at
+    // draft i's position if RoPE is on
+    auto load_row = [&](const float *src, int64_t i, bool turn, uint64_t *x) {
+      float f[2 * NP];
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j)
+        *reinterpret_cast<float4 *>(f + 4 * j) =
+            *reinterpret_cast<const float4 *>(src + (li + 8 * j) * 4);
+      if (turn && v.rope) {
+        const float2 *cs = tv.cs + i * (D / 2);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 w = cs[(li + 8 * j) * 4 + e];
+            const float c0 = f[4 * j + e], c1 = f[4 * (j + D / 64) + e];
+            f[4 * j + e] = c0 * w.x - c1 * w.y;
+            f[4 * (j + D / 64) + e] = c1 * w.x + c0 * w.y;
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < NP; ++j) x[j] = tc::f2_pack(f[2 * j], f[2 * j + 1]);
+    };
+    uint64_t q[kPerWarp][NP], o[kPerWarp][NP];
+    float m[kPerWarp], l[kPerWarp];
+    int limit[kPerWarp];
+    uint32_t above[kPerWarp];  // (16 drafts at most)
+#pragma unroll
+    for (int r = 0; r < kPerWarp; ++r) {
+      const int64_t i = draft0 + min(group * kPerWarp + r, n - 1);
+      load_row(a.q + (i * v.H + pc.h) * D, i, true, q[r]);
+      limit[r] = v.W - 1 - tv.depth[i];
+      above[r] = tv.above[i].x;
+      m[r] = -FLT_MAX;
+      l[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        q[r][j] = tc::fmul2(q[r][j], tc::f2_pack(qs, qs));
+        o[r][j] = 0;
+      }
+    }
+    // one key a lane group: scores, weights, and the value rows that are seen
+    auto score = [&](const uint64_t *k, float *x) {
+#pragma unroll
+      for (int r = 0; r < kPerWarp; ++r) {
+        uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+        for (int j = 0; j < NP; j += 2) {
+          s0 = tc::ffma2(q[r][j], k[j], s0);
+          s1 = tc::ffma2(q[r][j + 1], k[j + 1], s1);
+        }
+        s0 = tc::fadd2(s0, s1);
+        x[r] = tc::f2_lo(s0) + tc::f2_hi(s0);
+      }
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1)
+#pragma unroll
+        for (int r = 0; r < kPerWarp; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], off);
+    };
+    // seen: bit r, draft r sees the key; `all` if every bit of every lane is set
+    auto weigh = [&](float *x, uint32_t seen, bool all) {
+      bool grew = false;
+#pragma unroll
+      for (int r = 0; r < kPerWarp; ++r) {
+        if (!all && !((seen >> r) & 1u)) x[r] = -INFINITY;
+        grew |= x[r] - m[r] > kGrowth;
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int r = 0; r < kPerWarp; ++r)
+          if (x[r] - m[r] > kGrowth) {
+            const float f = exp2f(m[r] - x[r]);
+            m[r] = x[r];
+            l[r] *= f;
+#pragma unroll
+            for (int j = 0; j < NP; ++j) o[r][j] = tc::fmul2(o[r][j], tc::f2_pack(f, f));
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < kPerWarp; ++r) {
+        x[r] = exp2f(x[r] - m[r]);
+        l[r] += x[r];
+      }
+    };
+    auto gather = [&](const uint64_t *val, const float *w, uint32_t seen, bool all) {
+#pragma unroll
+      for (int r = 0; r < kPerWarp; ++r)
+        if (all || ((seen >> r) & 1u)) {  // an unseen entry's value never enters, whatever it holds
+#pragma unroll
+          for (int j = 0; j < NP; ++j) o[r][j] = tc::ffma2(val[j], tc::f2_pack(w[r], w[r]), o[r][j]);
+        }
+    };
+    auto from_smem = [&](const float *row, uint64_t *x) {
+#pragma unroll
+      for (int j = 0; j < NP; j += 2) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row + (li + 4 * j) * 4);
+        x[j] = u.x;
+        x[j + 1] = u.y;
+      }
+    };
+
+    if (pc.key_begin == 0) {
+      for (int j0 = wg * 4; j0 < n; j0 += kWarps * 4) {
+        const int key = j0 + lg;
+        const int64_t i = draft0 + min(key, n - 1);
+        uint32_t seen = 0;
+#pragma unroll
+        for (int r = 0; r < kPerWarp; ++r)
+          seen |= (key < n && ((above[r] >> key) & 1u) ? 1u : 0u) << r;
+        uint64_t row[NP];
+        float x[kPerWarp];
+        load_row(a.kd + (i * v.H + pc.h) * D, i, true, row);
+        score(row, x);
+        weigh(x, seen, false);
+        load_row(a.vd + (i * v.H + pc.h) * D, i, false, row);
+        gather(row, x, seen, false);
+      }
+    }
+    int k0, k1;
+    slots(pc, ring, k0, k1);
+    for (; k0 < k1; k0 += kRows, ++it) {
+      const int s = it % NST, rows = min(kRows, k1 - k0);
+      const bool all = !ring.swa && rows == kRows && k0 + kRows <= ring.plen;
+      if (!dead && !mbar_wait_bounded(&sm.full[s], (it / NST) & 1, v.err, RSWA_DEVERR_TIMEOUT))
+        dead = true;
+      dead = __any_sync(0xffffffffu, dead) != 0;
+      if (!dead) {
+#pragma unroll 1
+        for (int r0 = wg * 4; r0 < rows; r0 += kWarps * 4) {
+          const int key = min(r0 + lg, rows - 1);
+          uint32_t seen = 0xfu;
+          if (!all) {
+            const int age = r0 + lg < rows ? slot_age(ring, k0 + key) : INT_MAX;
+            seen = 0;
+#pragma unroll
+            for (int r = 0; r < kPerWarp; ++r) seen |= (age <= limit[r] ? 1u : 0u) << r;
+          }
+          uint64_t row[NP];
+          float x[kPerWarp];
+          from_smem(sm.k[s] + key * D, row);
+          score(row, x);
+          weigh(x, seen, all);
+          from_smem(sm.v[s] + key * D, row);
+          gather(row, x, seen, all);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[s]);
+    }
+
+    // the warp's four lane groups, then the group's warps
+#pragma unroll
+    for (int r = 0; r < kPerWarp; ++r) {
+      const float top = fmaxf(fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 8)),
+                              __shfl_xor_sync(0xffffffffu, fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 8)), 16));
+      const float f = exp2f(m[r] - top);
+      float lr = l[r] * f;
+      lr += __shfl_xor_sync(0xffffffffu, lr, 8);
+      lr += __shfl_xor_sync(0xffffffffu, lr, 16);
+      if (lane == 0) {
+        sm.red_m[warp][r] = top;
+        sm.red_l[warp][r] = lr;
+      }
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        float x = tc::f2_lo(o[r][j]) * f, y = tc::f2_hi(o[r][j]) * f;
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        y += __shfl_xor_sync(0xffffffffu, y, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        y += __shfl_xor_sync(0xffffffffu, y, 16);
+        if (lg == 0)
+          *reinterpret_cast<float2 *>(&sm.red_o[warp][r][(li + 8 * (j >> 1)) * 4 + (j & 1) * 2]) =
+              make_float2(x, y);
+      }
+    }
+    __syncwarp();
+    named_bar_sync(1, kRowWarps * 32);
+    for (int e = (int)threadIdx.x; e < G * kPerWarp * (D / 4); e += kRowWarps * 32) {
+      const int i = e / (D / 4), c = e % (D / 4) * 4;
+      if (i >= n) continue;
+      const int w0 = i / kPerWarp * kWarps, r = i % kPerWarp;
+      float top = -FLT_MAX;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.red_m[w0 + w][r]);
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2f(sm.red_m[w0 + w][r] - top);
+        const float4 x = *reinterpret_cast<const float4 *>(&sm.red_o[w0 + w][r][c]);
+        sum = fmaf(f, sm.red_l[w0 + w][r], sum);
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
+      }
+      if (pc.count == 1) {
+        *reinterpret_cast<float4 *>(a.out + ((draft0 + i) * v.H + pc.h) * D + c) =
+            make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum);
+      } else {
+        *reinterpret_cast<float4 *>(tv.part_o + ((int64_t)p * tv.T + i) * D + c) = acc;
+        if (c == 0)
+          tv.part_ml[(int64_t)p * tv.T + i] =
+              make_float2(top == -FLT_MAX ? -INFINITY : top, sum);
+      }
+    }
+    __syncwarp();
+    named_bar_sync(1, kRowWarps * 32);  // the partials are read
+  }
 }
 
-template <int D, int kRows>
-cudaError_t launch_t(const TreeSimtArgs &a, cudaStream_t s) {
-  cudaError_t e = set_attr<D, kRows>();
+template <typename Smem>
+cudaError_t prepare_kernel(void (*kernel)(TreeSimtArgs)) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(Smem));
+}
+
+template <int D, int G>
+cudaError_t launch_rows(const TreeSimtArgs &a, cudaStream_t s) {
+  cudaError_t e = prepare_kernel<RowsSmem<D>>(tree_rows_kernel<D, G>);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + kRows - 1) / kRows));
-  return launch_overlapped(tree_simt_kernel<D, kRows>, grid, dim3(kThreads),
-                           sizeof(SimtSmem<D, kRows>), s, a);
+  return launch_overlapped(tree_rows_kernel<D, G>, dim3((unsigned)a.tv.grid),
+                           dim3((kRowWarps + 1) * 32), sizeof(RowsSmem<D>), s, a);
 }
 
-template <int D, int kRows>
-int ctas_t() {
+template <int D>
+cudaError_t launch_d(const TreeSimtArgs &a, cudaStream_t s) {
+  if (a.tv.T <= 4) return launch_rows<D, 1>(a, s);
+  if (a.tv.T <= 8) return launch_rows<D, 2>(a, s);
+  if (a.tv.T <= kRowsMax) return launch_rows<D, 4>(a, s);
+  cudaError_t e = prepare_kernel<SimtSmem<D, 64>>(tree_simt_kernel<D, 64>);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + 63) / 64));
+  return launch_overlapped(tree_simt_kernel<D, 64>, grid, dim3(kThreads), sizeof(SimtSmem<D, 64>),
+                           s, a);
+}
+
+template <int D>
+int ctas_d(int n_rows) {
+  if (n_rows <= kRowsMax) return 1;  // 176 KB of shared memory
   int n = 0;
-  if (set_attr<D, kRows>() != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, tree_simt_kernel<D, kRows>, kThreads,
-                                                    sizeof(SimtSmem<D, kRows>)) != cudaSuccess ||
+  if (prepare_kernel<SimtSmem<D, 64>>(tree_simt_kernel<D, 64>) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, tree_simt_kernel<D, 64>, kThreads,
+                                                    sizeof(SimtSmem<D, 64>)) != cudaSuccess ||
       n < 1)
     return 1;
   return n;
@@ -303,18 +618,14 @@ int ctas_t() {
 }  // namespace
 
 int tree_simt_ctas_per_sm(int head_dim, int n_rows) {
-  const bool small = n_rows <= 16;
-  if (head_dim == 128) return small ? ctas_t<128, 16>() : ctas_t<128, 64>();
-  return small ? ctas_t<64, 16>() : ctas_t<64, 64>();
+  return head_dim == 128 ? ctas_d<128>(n_rows) : ctas_d<64>(n_rows);
 }
 
 cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const float *q,
                              const float *kd, const float *vd, const float *kc, const float *vc,
                              float *out, cudaStream_t s) {
   const TreeSimtArgs a{v, tv, q, kd, vd, kc, vc, out};
-  const bool small = tv.T <= 16;
-  if (v.D == 128) return small ? launch_t<128, 16>(a, s) : launch_t<128, 64>(a, s);
-  return small ? launch_t<64, 16>(a, s) : launch_t<64, 64>(a, s);
+  return v.D == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
 }
 
 }  // namespace rswa
