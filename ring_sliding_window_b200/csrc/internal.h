@@ -65,7 +65,8 @@ constexpr int kTopkMaxWindow = 8192;         // history staged in shared memory
 constexpr int kTreeTcTile = 128;    // keys per tile of the tensor-core tree kernel
 constexpr int kTreeTcRows = 64;     // drafts that a CTA of it takes
 constexpr int kTreeTcPieceCost = 2; // tiles that a piece's beginning and end cost
-constexpr int kTreeSimtTile = 64;   // keys per tile of the FP32 tree kernel
+constexpr int kTreeSimtTile = 64;   // keys per tile of the FP32 tree kernels
+constexpr int kTreeSimtPieceCost = 1;
 constexpr int kPrefillTile = 128;  // query rows per prefill tile (tensor-core kernel)
 constexpr int kSimtTile = 64;      // query rows per prefill tile (FP32 SIMT kernel)
 
@@ -207,8 +208,8 @@ cudaError_t launch_tree_rope(const DeviceView &v, const TreeView &tv, cudaStream
 cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const float *q,
                              const float *kd, const float *vd, const float *kc, const float *vc,
                              float *out, cudaStream_t s);
-// CTAs of the FP32 kernel that one SM holds.
-int tree_simt_ctas_per_sm(int head_dim, int n_rows);
+// CTAs in a row of the FP32 kernels' grid for trees of T.
+int tree_simt_ctas(int num_sms, int head_dim, int T);
 // The tensor-core form (bf16), and the tensor maps over one layer's caches that
 // it takes (cache_rows rows of d elements); false if they cannot be made.
 bool tree_tc_maps(const DeviceView &v, const void *kc, const void *vc, int64_t cache_rows,

@@ -349,8 +349,8 @@ DecodePlan plan_for(const rswa_state *s, int T) {
     const int cols = (T + kTreeTcRows - 1) / kTreeTcRows;
     return plan_tree(s, T, kTreeTcTile, std::max(1, s->num_sms / cols), kTreeTcPieceCost);
   }
-  return plan_tree(s, T, kTreeSimtTile, s->num_sms * tree_simt_ctas_per_sm(s->cfg.head_dim, T),
-                   0);
+  return plan_tree(s, T, kTreeSimtTile,
+                   std::max(1, tree_simt_ctas(s->num_sms, s->cfg.head_dim, T)), kTreeSimtPieceCost);
 }
 
 struct TreeLayout {

@@ -9,16 +9,18 @@
 // tiles per CTA (the work plan of the tree); a ring in several pieces leaves
 // partials that tree_combine_kernel merges.
 //
-// Up to 16 drafts: tree_rows_kernel.  A warp takes four drafts, their queries
-// and outputs in registers, and four keys at a time, 8 lanes a key; a producer
-// warp streams K and V rows into shared memory by bulk copies.  Every 16 bytes
-// that leave shared memory meet four drafts, in packed FP32 pairs, so HBM stays
-// the bound up to 8 drafts and FMA issue is close to it at 16.
+// Up to 32 drafts: tree_rows_kernel, 16 of them a CTA.  A warp takes four drafts,
+// their queries and outputs in registers, and four keys at a time, 8 lanes a key;
+// a producer warp streams K and V rows into shared memory by bulk copies.  Every
+// 16 bytes that leave shared memory meet four drafts, in packed FP32 pairs.  Bound
+// by HBM up to 4 drafts (8 x 8,000 tokens, d = 128: 118 us, 87 % of the measured
+// copy rate), by instruction issue from 8 (4 x 4,096 tokens, 16 drafts: 101 us).
 //
 // More: tree_simt_kernel, row groups of 64.  A tile is 64 keys: 256 threads form
 // a 16 x 16 grid, each with 4 query rows x 4 keys of the scores, then the same
 // rows x D / 16 output columns.  Bound by FP32 FMA issue and the barriers between
-// its phases.
+// its phases (4 x 4,096 tokens: 32 drafts would take 235 us for the rows
+// kernel's 186, 64 take 239 for its 373).
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
@@ -34,11 +36,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKeys = kTreeSimtTile;
 constexpr int kThreads = 256;
-constexpr int kRowsMax = 16;      // drafts that tree_rows_kernel takes
+constexpr int kRowsMax = 32;      // drafts that tree_rows_kernel takes
+constexpr int kRowsCta = 16;      // of them a CTA
 constexpr float kMasked = -1.f;  // marks an unseen pair where a weight (>= 0) would stand
 
-template <int D, int kRows>
+template <int D>
 struct SimtSmem {
+  static constexpr int kRows = 64;
   float q[kRows][D + 4];
   float k[kKeys][D + 4];
   float v[kKeys][D + 4];
@@ -80,11 +84,12 @@ __device__ __forceinline__ void load_rotated(const float *src, float *dst, int c
   *reinterpret_cast<float4 *>(dst + c * N + D / 2) = make_float4(b[0], b[1], b[2], b[3]);
 }
 
-template <int D, int kRows>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
     tree_simt_kernel(const TreeSimtArgs a) {
-  using Smem = SimtSmem<D, kRows>;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  using Smem = SimtSmem<D>;
+  constexpr int kRows = Smem::kRows;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
   constexpr int kRT = kRows / 16;       // rows of a thread
   constexpr int kCT = D / 64;           // groups of 4 output columns of a thread
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// ------------------------------------------------------- up to 16 drafts
+// ------------------------------------------------------- up to 32 drafts
 constexpr int kRowWarps = 8;            // consumer warps
 constexpr int kPerWarp = 4;             // drafts of a warp
 constexpr float kGrowth = 8.f;          // m moves past a score 2^8 above it
@@ -309,6 +314,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
   const DeviceView &v = a.v;
   const TreeView &tv = a.tv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = (int)blockIdx.y * kRowsCta;  // this CTA's first draft
   const int p_begin = tv.cta_piece[blockIdx.x], p_end = tv.cta_piece[blockIdx.x + 1];
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
     bool ok = true;
     for (int p = p_begin; ok && p < p_end; ++p) {
       const DecodePiece pc = tv.pieces[p];
-      if (tv.n[pc.b] == 0) continue;
+      if (tv.n[pc.b] <= row0) continue;
       const RingView ring = ring_view(v, pc.b, pc.plen);
       int k0, k1;
       slots(pc, ring, k0, k1);
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
   for (int p = p_begin; p < p_end; ++p) {
     const DecodePiece pc = tv.pieces[p];
     const int n = tv.n[pc.b];
-    if (n == 0) continue;
+    if (n <= row0) continue;
     const RingView ring = ring_view(v, pc.b, pc.plen);
     const int64_t draft0 = (int64_t)pc.b * tv.T;
     // a row's chunks li, li + 8, ... (16 bytes each) as packed pairs, turned at
@@ -392,10 +398,10 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
     uint64_t q[kPerWarp][NP], o[kPerWarp][NP];
     float m[kPerWarp], l[kPerWarp];
     int limit[kPerWarp];
-    uint32_t above[kPerWarp];  // (16 drafts at most)
+    uint32_t above[kPerWarp];  // (32 drafts at most)
 #pragma unroll
     for (int r = 0; r < kPerWarp; ++r) {
-      const int64_t i = draft0 + min(group * kPerWarp + r, n - 1);
+      const int64_t i = draft0 + min(row0 + group * kPerWarp + r, n - 1);
       load_row(a.q + (i * v.H + pc.h) * D, i, true, q[r]);
       limit[r] = v.W - 1 - tv.depth[i];
       above[r] = tv.above[i].x;
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
     named_bar_sync(1, kRowWarps * 32);
     for (int e = (int)threadIdx.x; e < G * kPerWarp * (D / 4); e += kRowWarps * 32) {
       const int i = e / (D / 4), c = e % (D / 4) * 4;
-      if (i >= n) continue;
+      if (row0 + i >= n) continue;
       const int w0 = i / kPerWarp * kWarps, r = i % kPerWarp;
       float top = -FLT_MAX;
 #pragma unroll
@@ -563,12 +569,12 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
         acc.w = fmaf(f, x.w, acc.w);
       }
       if (pc.count == 1) {
-        *reinterpret_cast<float4 *>(a.out + ((draft0 + i) * v.H + pc.h) * D + c) =
+        *reinterpret_cast<float4 *>(a.out + ((draft0 + row0 + i) * v.H + pc.h) * D + c) =
             make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum);
       } else {
-        *reinterpret_cast<float4 *>(tv.part_o + ((int64_t)p * tv.T + i) * D + c) = acc;
+        *reinterpret_cast<float4 *>(tv.part_o + ((int64_t)p * tv.T + row0 + i) * D + c) = acc;
         if (c == 0)
-          tv.part_ml[(int64_t)p * tv.T + i] =
+          tv.part_ml[(int64_t)p * tv.T + row0 + i] =
               make_float2(top == -FLT_MAX ? -INFINITY : top, sum);
       }
     }
@@ -587,8 +593,9 @@ template <int D, int G>
 cudaError_t launch_rows(const TreeSimtArgs &a, cudaStream_t s) {
   cudaError_t e = prepare_kernel<RowsSmem<D>>(tree_rows_kernel<D, G>);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(tree_rows_kernel<D, G>, dim3((unsigned)a.tv.grid),
-                           dim3((kRowWarps + 1) * 32), sizeof(RowsSmem<D>), s, a);
+  const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + kRowsCta - 1) / kRowsCta));
+  return launch_overlapped(tree_rows_kernel<D, G>, grid, dim3((kRowWarps + 1) * 32),
+                           sizeof(RowsSmem<D>), s, a);
 }
 
 template <int D>
@@ -596,20 +603,19 @@ cudaError_t launch_d(const TreeSimtArgs &a, cudaStream_t s) {
   if (a.tv.T <= 4) return launch_rows<D, 1>(a, s);
   if (a.tv.T <= 8) return launch_rows<D, 2>(a, s);
   if (a.tv.T <= kRowsMax) return launch_rows<D, 4>(a, s);
-  cudaError_t e = prepare_kernel<SimtSmem<D, 64>>(tree_simt_kernel<D, 64>);
+  cudaError_t e = prepare_kernel<SimtSmem<D>>(tree_simt_kernel<D>);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + 63) / 64));
-  return launch_overlapped(tree_simt_kernel<D, 64>, grid, dim3(kThreads), sizeof(SimtSmem<D, 64>),
-                           s, a);
+  constexpr int kRows = SimtSmem<D>::kRows;
+  const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + kRows - 1) / kRows));
+  return launch_overlapped(tree_simt_kernel<D>, grid, dim3(kThreads), sizeof(SimtSmem<D>), s, a);
 }
 
 template <int D>
-int ctas_d(int n_rows) {
-  if (n_rows <= kRowsMax) return 1;  // 176 KB of shared memory
+int ctas_d() {
   int n = 0;
-  if (prepare_kernel<SimtSmem<D, 64>>(tree_simt_kernel<D, 64>) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, tree_simt_kernel<D, 64>, kThreads,
-                                                    sizeof(SimtSmem<D, 64>)) != cudaSuccess ||
+  if (prepare_kernel<SimtSmem<D>>(tree_simt_kernel<D>) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, tree_simt_kernel<D>, kThreads,
+                                                    sizeof(SimtSmem<D>)) != cudaSuccess ||
       n < 1)
     return 1;
   return n;
@@ -617,8 +623,10 @@ int ctas_d(int n_rows) {
 
 }  // namespace
 
-int tree_simt_ctas_per_sm(int head_dim, int n_rows) {
-  return head_dim == 128 ? ctas_d<128>(n_rows) : ctas_d<64>(n_rows);
+int tree_simt_ctas(int num_sms, int head_dim, int T) {
+  // the rows kernel: one CTA an SM, its columns of the grid side by side
+  if (T <= kRowsMax) return num_sms / ((T + kRowsCta - 1) / kRowsCta);
+  return num_sms * (head_dim == 128 ? ctas_d<128>() : ctas_d<64>());
 }
 
 cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const float *q,
