@@ -11,7 +11,7 @@ import importlib
 
 
 def __getattr__(name):
-    if name.startswith(("rswa_", "RSWA_", "Rswa")) or name in ("State", "Config", "lib"):
+    if name.startswith(("rswa_", "RSWA_", "Rswa")) or name in ("State", "Tree", "Config", "lib"):
         mod = importlib.import_module(".rswa", __name__)
         return getattr(mod, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -68,11 +68,11 @@ __global__ void __launch_bounds__(kFinishThreads)
 // memory (beyond kSelCache entries they are read again, from L2), and every loop
 // after the first takes four a thread.
 //
-// Bound by instruction issue (about 40 an entry and lane over five loops) and,
-// for short rings, by the latency of seven short phases.  TODO us for 80 rings of
-// 8,256 entries, TODO us for 40 of 32,640.  Clusters of 2 and 4 CTAs a ring that add
-// their counts through distributed shared memory took longer: what their
-// barriers and remote loads cost is more than the loops.
+// Bound by instruction issue (about 100 an entry and lane over five loops) and,
+// for short rings, by the latency of seven short phases: 19 us for 40 rings of
+// 32,640 entries, 9 us for 80 of 8,256.  Clusters of 2 and 4 CTAs a ring, adding
+// their counts through distributed shared memory, cost 10 us more: their barriers
+// and remote loads take longer than the loops that they share.
 constexpr int kSelMaxThreads = 1024;
 constexpr int kSelBins = 2048;
 constexpr int kSelCache = 49152;  // 192 KB
@@ -95,29 +95,6 @@ __device__ __forceinline__ uint32_t score_key(float x, bool guarded) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 constexpr uint32_t kZeroKey = 0x80000000u;
-
-// Counts of bins: a thread's runs of one bin (equal scores, protected entries)
-// and its exact zeros, which are many, take one shared atomic each.
-struct BinCounter {
-  uint32_t *hist;
-  uint32_t bin = 0, run = 0, zeros = 0;
-  __device__ __forceinline__ void add(uint32_t b, bool zero) {
-    if (zero) {
-      ++zeros;
-    } else if (b == bin) {
-      ++run;
-    } else {
-      if (run) atomicAdd(&hist[bin], run);
-      bin = b;
-      run = 1;
-    }
-  }
-  __device__ __forceinline__ void finish(uint32_t zero_bin) {
-    if (run) atomicAdd(&hist[bin], run);
-    zeros = __reduce_add_sync(0xffffffffu, zeros);
-    if ((threadIdx.x & 31) == 0 && zeros) atomicAdd(&hist[zero_bin], zeros);
-  }
-};
 
 __global__ void __launch_bounds__(kSelMaxThreads)
     evict_select_kernel(const SelectArgs a) {
@@ -164,7 +141,13 @@ __global__ void __launch_bounds__(kSelMaxThreads)
     shift -= bits;
     for (int i = tid; i < (int)bins; i += nt) hist[i] = 0;
     __syncthreads();
-    BinCounter counter{hist};
+    // exact zeros are many and share a bin: counted by the thread
+    uint32_t zeros = 0;
+    auto count = [&](uint32_t k, bool in) {
+      const bool zero = k == kZeroKey;
+      zeros += in && zero ? 1u : 0u;
+      if (in && !zero) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+    };
     if (pass == 0) {
       for (int s0 = tid; s0 < P; s0 += kSelAhead * nt) {
         float x[kSelAhead];
@@ -173,26 +156,27 @@ __global__ void __launch_bounds__(kSelMaxThreads)
 #pragma unroll
         for (int u = 0; u < kSelAhead; ++u) {
           const int s = s0 + u * nt;
-          if (s < P) {
-            const uint32_t k = to_key(x[u], s);
-            if (s < a.cache) keys[s] = k;
-            counter.add(k >> shift, k == kZeroKey);
-          }
+          const uint32_t k = to_key(x[u], s);
+          if (s < min(P, a.cache)) keys[s] = k;
+          count(k, s < P);
         }
       }
     } else {
-#pragma unroll 2
+#pragma unroll 4
       for (int i = tid; i < quads; i += nt) {
         const uint4 q = key4(i);
         const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+        bool in[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if ((k[c] >> above) == prefix && 4 * i + c < P)
-            counter.add((k[c] >> shift) & (bins - 1), k[c] == kZeroKey);
+        for (int c = 0; c < 4; ++c) in[c] = (k[c] >> above) == prefix && 4 * i + c < P;
+        if (in[0] || in[1] || in[2] || in[3])
+#pragma unroll
+          for (int c = 0; c < 4; ++c) count(k[c], in[c]);
       }
     }
     __syncwarp();
-    counter.finish((kZeroKey >> shift) & (bins - 1));
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if (lane == 0 && zeros) atomicAdd(&hist[(kZeroKey >> shift) & (bins - 1)], zeros);
     __syncthreads();
     // bins from the highest down, bins / nt of them a thread
     const int per = (int)bins / nt;
@@ -229,9 +213,8 @@ __global__ void __launch_bounds__(kSelMaxThreads)
   const int span = ((quads + 31) / 32 + warps - 1) / warps * 32;  // quads of a warp
   const int i0 = warp * span, i1 = min((quads + 31) / 32 * 32, i0 + span);
   uint32_t gt = 0, eq = 0;
-#pragma unroll 2
-  for (int i = i0 + lane; i < i1; i += 32) {
-    if (i >= quads) break;
+#pragma unroll 4
+  for (int i = i0 + lane; i < min(i1, quads); i += 32) {
     const uint4 q = key4(i);
     const uint32_t k[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -252,29 +235,33 @@ __global__ void __launch_bounds__(kSelMaxThreads)
   // entries above and at the threshold before this warp's next 128
   uint32_t g = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0u);
   uint32_t e = __reduce_add_sync(0xffffffffu, lane < warp ? warp_b[lane] : 0u);
+#pragma unroll 4
   for (int i = i0 + lane; i < i1; i += 32) {
     const uint4 q = i < quads ? key4(i) : make_uint4(0u, 0u, 0u, 0u);
     const uint32_t k[4] = {q.x, q.y, q.z, q.w};
-    uint32_t mine = 0;  // above the threshold, and at it in the upper half
+    uint32_t mine = 0, each[4];  // above the threshold, and at it in the upper half
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (4 * i + c < P) mine += k[c] > thr ? 1u : k[c] == thr ? 0x10000u : 0u;
+    for (int c = 0; c < 4; ++c) {
+      each[c] = k[c] > thr ? 1u : k[c] == thr ? 0x10000u : 0u;
+      if (4 * i + c >= P) each[c] = 0u;
+      mine += each[c];
+    }
     uint32_t run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t up = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += up;
+      run += lane >= o ? up : 0u;
     }
     const uint32_t all = __shfl_sync(0xffffffffu, run, 31);
     uint32_t my_g = g + ((run - mine) & 0xffffu), my_e = e + ((run - mine) >> 16);
+    if (mine)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (4 * i + c >= P || k[c] < thr) continue;
-      const bool is_gt = k[c] > thr;
-      if (is_gt || my_e < left) a.kept[list0 + my_g + min(my_e, left)] = 4 * i + c;
-      my_g += is_gt ? 1u : 0u;
-      my_e += is_gt ? 0u : 1u;
-    }
+      for (int c = 0; c < 4; ++c) {
+        if (each[c] == 1u || (each[c] && my_e < left))
+          a.kept[list0 + my_g + min(my_e, left)] = 4 * i + c;
+        my_g += each[c] & 1u;
+        my_e += each[c] >> 16;
+      }
     g += all & 0xffffu;
     e += all >> 16;
   }

@@ -378,8 +378,8 @@ def rswa_tree_attention(tree, layer, q, k_draft, v_draft, out, stream=None) -> N
 
 def rswa_tree_commit(tree, k_draft, v_draft, path, path_len, stream=None) -> None:
     """k_draft, v_draft: one tensor a layer; path: cuda int32 [B, T]; path_len: cuda int32 [B]."""
-    kp = (ctypes.c_void_p * len(k_draft))(*[_ptr(t) for t in k_draft])
-    vp = (ctypes.c_void_p * len(v_draft))(*[_ptr(t) for t in v_draft])
+    kp = (ctypes.c_void_p * len(k_draft))(*map(_ptr, k_draft))
+    vp = (ctypes.c_void_p * len(v_draft))(*map(_ptr, v_draft))
     _check(lib.rswa_tree_commit(tree, kp, vp, _ptr(path), _ptr(path_len), _stream(stream)),
            "rswa_tree_commit")
 
@@ -621,8 +621,9 @@ class Tree:
         st = self.state
         if len(k_draft) != st.L or len(v_draft) != st.L:
             raise RswaError(RSWA_EINVAL, "commit: needs one k_draft and one v_draft a layer")
+        shape, dtype, device = self._shape, st.dtype, st._device
         for t in (*k_draft, *v_draft):
-            self._drafts(t, "draft")
+            _require(t, "draft", shape, dtype, device)
         _require(path, "path", (st.B, self.T), torch.int32, st._device)
         _require(path_len, "path_len", (st.B,), torch.int32, st._device)
         rswa_tree_commit(self.handle, k_draft, v_draft, path, path_len, stream)
