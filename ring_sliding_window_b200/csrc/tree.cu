@@ -36,7 +36,8 @@ namespace {
 // One CTA per sequence, one thread per node.  Depths and the sets of nodes
 // above each node come from pointer doubling: with up(i) the 2^k-th node above
 // i and above(i) the set of the first 2^k, above(i) |= above(up(i)) doubles k;
-// seven rounds reach 128.  Latency-bound (a few kilobytes of input).
+// seven rounds reach 128, fewer the deepest node.  The sets below a node are the
+// transpose.  Latency-bound (a few kilobytes of input).
 __global__ void __launch_bounds__(RSWA_TREE_MAX)
     tree_set_kernel(const DeviceView v, const TreeView tv, const int32_t *parent,
                     const int32_t *n_draft) {
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(RSWA_TREE_MAX)
   int cur = 0;
 #pragma unroll 1
   for (int k = 0; k < 7; ++k) {
+    if (!__syncthreads_or(up[cur][i] >= 0)) break;  // every path has reached its top
     const int u = up[cur][i], nx = cur ^ 1;
     const bool some = u >= 0;
     for (int w = 0; w < 4; ++w) above[nx][i][w] = above[cur][i][w] | (some ? above[cur][u][w] : 0u);
@@ -84,15 +86,29 @@ __global__ void __launch_bounds__(RSWA_TREE_MAX)
     for (int j = 0; j < i; ++j)
       if (depth[cur][j] < d - v.W + 1) above[cur][i][j >> 5] &= ~(1u << (j & 31));
   }
+  __shared__ uint4 below[RSWA_TREE_MAX];
+  {
+    // 32 x 32 bits at a time: lane l takes column l of its warp's rows
+    const int lane = i & 31;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t x = i < n ? above[cur][i][c] : 0u;
+      uint32_t m = 0x0000ffffu;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, x, o);
+        x = lane & o ? (x & ~m) | ((y >> o) & m) : (x & m) | ((y << o) & ~m);
+        m ^= m << (o >> 1);
+      }
+      reinterpret_cast<uint32_t *>(&below[32 * c + lane])[i >> 5] = x;
+    }
+  }
   __syncthreads();
   if (i >= T) return;
-  uint32_t below[4] = {0u, 0u, 0u, 0u};
-  for (int j = i; j < n; ++j)  // a draft's row number is above its ancestors'
-    below[j >> 5] |= ((above[cur][j][i >> 5] >> (i & 31)) & 1u) << (j & 31);
   const int64_t row = (int64_t)b * T + i;
   tv.parent[row] = pr;
   tv.depth[row] = d;
-  tv.below[row] = make_uint4(below[0], below[1], below[2], below[3]);
+  tv.below[row] = below[i];
   tv.above[row] = make_uint4(above[cur][i][0], above[cur][i][1], above[cur][i][2], above[cur][i][3]);
 }
 
