@@ -520,6 +520,7 @@ rswa_status rswa_tree_attention(rswa_tree *tree, int32_t layer, const void *q, c
   const rswa_state *s = tree->state;
   if (layer < 0 || layer >= s->cfg.num_layers) return RSWA_EINVAL;
   if (!q || !k_draft || !v_draft || !out) return RSWA_EINVAL;
+  if (out == q || out == k_draft || out == v_draft) return RSWA_EINVAL;
   if (!aligned16(q) || !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out))
     return RSWA_EINVAL;
   if (!s->layer_ready[(size_t)layer]) return RSWA_ESTATE;

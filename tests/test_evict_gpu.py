@@ -196,6 +196,32 @@ def test_evict_orders_every_float():
         _check_evicted(src, dst, 0, score, out, kept, 1, 2, (2,), H)
 
 
+@pytest.mark.parametrize("P", [49151, 49152, 49157, 120001])
+def test_evict_from_long_prompts(P):
+    """Prompts around and beyond what a CTA's shared memory holds: many values, and ties."""
+    rswa = _rswa()
+    H, W, first, last = 2, 3, 5, 70
+    for keep in (100, P // 3, P - 1):
+        src = rswa.State(1, 1, H, 64, W, (P,), dtype=BF, n_generated=(2,))
+        dst = rswa.State(1, 1, H, 64, W, (keep,), dtype=BF)
+        _fill_random(src, BF, 1, 1)
+        for kind in range(3):
+            score = torch.rand(src.score_buffer().numel(), device="cuda").pow(6) - 0.2
+            if kind == 1:
+                score = (score * 8).round() / 8
+            if kind == 2:
+                score[torch.rand_like(score) < 0.9] = 0.0
+            kept = src.evict_into(dst, 0, score, first, last).view(H, keep)
+            for h in range(H):
+                rank = src.score_view(score, 0, h)[:P].clone()
+                rank[:first] = rank[P - last:] = float("inf")
+                order = torch.sort(rank, descending=True, stable=True).indices[:keep]
+                want = torch.sort(order).values
+                assert torch.equal(kept[h].long(), want)
+                assert torch.equal(_bits(dst.cache_view(0, "k", 0, h)[:keep]),
+                                   _bits(src.cache_view(0, "k", 0, h)[want]))
+
+
 def test_all_scores_equal_keeps_the_first_slots():
     rswa = _rswa()
     P, keep, H = 20000, 7777, 2

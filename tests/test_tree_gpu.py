@@ -397,6 +397,29 @@ def test_commit_writes_the_path_and_nothing_else(dtype, d):
     assert c.st.check() == 0
 
 
+def test_commit_into_many_layers():
+    """More layers than one launch takes, every one with its own drafts."""
+    rswa = _rswa()
+    L, H, d, W, P, T, t = 67, 1, 64, 5, 3, 4, 6
+    st = rswa.State(1, L, H, d, W, (P,), dtype=BF, n_generated=(t,))
+    for x in st.k_cache + st.v_cache:
+        x.fill_(1.0)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ks, vs = ([torch.randn(1, T, H, d, generator=g, device="cuda").to(BF) for _ in range(L)]
+              for _ in range(2))
+    tree = st.tree(T)
+    tree.set()
+    tree.commit(ks, vs, _ints([[0, 1, 2, 0]]), _ints([3]))
+    tree.advance()
+    assert st.check() == 0 and st.ring()[0] == [t + 3]
+    for layer in range(L):
+        for w, src in (("k", ks), ("v", vs)):
+            want = torch.ones(P + W, d, dtype=BF, device="cuda")
+            for i in range(3):
+                want[P + (t + i) % W] = src[layer][0, i, 0]
+            assert torch.equal(st.cache_view(layer, w, 0, 0), want)
+
+
 def test_bad_trees_and_paths_are_refused_sequence_by_sequence():
     rswa = _rswa()
     T, W = 6, 8
@@ -525,7 +548,8 @@ def test_refusals():
     assert e.value.status == rswa.RSWA_ENOMEM
     bad = [(1, q, k, v, out), (-1, q, k, v, out), (0, q[:, :2], k, v, out),
            (0, q.float(), k, v, out), (0, q.cpu(), k, v, out),
-           (0, q.transpose(1, 2).contiguous().transpose(1, 2), k, v, out)]
+           (0, q.transpose(1, 2).contiguous().transpose(1, 2), k, v, out),
+           (0, q, k, v, q), (0, q, k, v, k), (0, q, k, v, v)]
     for args in bad:
         with pytest.raises(rswa.RswaError) as e:
             c.tree.attention(*args)
