@@ -134,51 +134,59 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   allow_dependents();
   if (p1 - p0 < 2) return;  // its one piece wrote the output
   const int b = (int)(bh / v.H), h = (int)(bh % v.H);
-  if (i >= tv.n[b]) return;
+  // one trip to memory: the count, 32 pieces' (m, l) and the first eight pieces' o
+  // at once (what the partials of absent rows and unseen pieces hold is not used)
+  const int n = tv.n[b];
+  const float *o_row = tv.part_o + (int64_t)i * D + lane * E;
+  const int64_t o_step = (int64_t)tv.T * D;
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int c0 = p0; c0 < p1; c0 += 32) {
     const int cnt = min(32, p1 - c0);
-    const float2 ml = lane < cnt ? tv.part_ml[(int64_t)(c0 + lane) * tv.T + i]
-                                 : make_float2(-INFINITY, 0.f);
+    float2 ml = tv.part_ml[(int64_t)(c0 + min(lane, cnt - 1)) * tv.T + i];
+    float o[kMergeAhead][E];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int u = 0; u < kMergeAhead; ++u) {
+        const float *src = o_row + (c0 + min(j0 + u, cnt - 1)) * o_step;
+        if constexpr (E == 4)
+          *reinterpret_cast<float4 *>(o[u]) = *reinterpret_cast<const float4 *>(src);
+        else
+          *reinterpret_cast<float2 *>(o[u]) = *reinterpret_cast<const float2 *>(src);
+      }
+    };
+    load(0);
+    if (i >= n) return;
+    if (lane >= cnt) ml = make_float2(-INFINITY, 0.f);
     // a piece in which the row saw nothing has no o; one of NaN scores has l = NaN
     const bool seen = ml.x != -INFINITY || ml.y != 0.f;
     float top = ml.x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int f = 16; f > 0; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
     const float m_new = fmaxf(m, top);
     const float w = !seen ? 0.f : ml.x == m_new ? 1.f : exp2f(ml.x - m_new);
     float lc = seen ? w * ml.y : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lc += __shfl_xor_sync(0xffffffffu, lc, o);
+    for (int f = 16; f > 0; f >>= 1) lc += __shfl_xor_sync(0xffffffffu, lc, f);
     const float corr = m == m_new ? 1.f : exp2f(m - m_new);
     l = fmaf(l, corr, lc);
     m = m_new;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= corr;
     const uint32_t use = __ballot_sync(0xffffffffu, seen);
-    for (int j0 = 0; j0 < cnt; j0 += kMergeAhead) {
-      float o[kMergeAhead][E];
-#pragma unroll
-      for (int u = 0; u < kMergeAhead; ++u) {
-        const float *src = tv.part_o + ((int64_t)(c0 + j0 + u) * tv.T + i) * D + lane * E;
-        if (j0 + u < 32 && ((use >> ((j0 + u) & 31)) & 1u)) {
-          if constexpr (E == 4)
-            *reinterpret_cast<float4 *>(o[u]) = *reinterpret_cast<const float4 *>(src);
-          else
-            *reinterpret_cast<float2 *>(o[u]) = *reinterpret_cast<const float2 *>(src);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[u][e] = 0.f;
-        }
-      }
+    for (int j0 = 0;;) {
 #pragma unroll
       for (int u = 0; u < kMergeAhead; ++u) {
         const float wj = __shfl_sync(0xffffffffu, w, (j0 + u) & 31);
+        if ((use >> ((j0 + u) & 31)) & 1u) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wj, o[u][e], acc[e]);
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wj, o[u][e], acc[e]);
+        }
       }
+      j0 += kMergeAhead;
+      if (j0 >= cnt) break;
+      load(j0);
     }
   }
   T *dst = out + (((int64_t)b * tv.T + i) * v.H + h) * D + lane * E;

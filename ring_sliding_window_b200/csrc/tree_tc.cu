@@ -314,11 +314,17 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     sm.dead = 0;
     fence_mbar_init();
   }
+  // the plan and the maps are the tree's own; the first tiles' way to L2, and that
+  // of the counters, can begin while the kernel before this one still runs (a hint
+  // returns nothing)
+  const DecodePiece first_piece = tv.pieces[p_begin];
   if (warp == kProducer && lane == 0) {
-    // the plan and the maps are the tree's own; the first tiles' way to L2 can
-    // begin while the kernel before this one still runs (a hint returns nothing)
-    const DecodePiece pc = tv.pieces[p_begin];
+    const DecodePiece &pc = first_piece;
+    prefetch_l2(tv.n + pc.b);
+    prefetch_l2(v.t + pc.b);
     tc::prefetch_tmap(&tm_q);
+    tc::prefetch_tmap(&tm_kd);
+    tc::prefetch_tmap(&tm_vd);
     tc::prefetch_tmap(&tm_kc);
     tc::prefetch_tmap(&tm_vc);
     const int first = max(0, pc.key_begin - 1);
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
       int it = 0, active = 0;
       bool ok = true;
       for (int p = p_begin; ok && p < p_end; ++p) {
-        const DecodePiece pc = tv.pieces[p];
+        const DecodePiece pc = p == p_begin ? first_piece : tv.pieces[p];
         if (tv.n[pc.b] <= row0) continue;
         const RingView ring = ring_view(v, pc.b, pc.plen);
         const PieceTiles pt(pc, ring);
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
       return true;
     };
     for (int p = p_begin; ok && p < p_end; ++p) {
-      const DecodePiece pc = tv.pieces[p];
+      const DecodePiece pc = p == p_begin ? first_piece : tv.pieces[p];
       if (tv.n[pc.b] <= row0) continue;
       const RingView ring = ring_view(v, pc.b, pc.plen);
       const PieceTiles pt(pc, ring);
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
       last = -1;
     };
     for (int p = p_begin; p < p_end; ++p) {
-      const DecodePiece pc = tv.pieces[p];
+      const DecodePiece pc = p == p_begin ? first_piece : tv.pieces[p];
       const int n = tv.n[pc.b];
       if (n <= row0) continue;
       const RingView ring = ring_view(v, pc.b, pc.plen);
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     };
     int it = 0, active = 0;
     for (int p = p_begin; p < p_end; ++p) {
-      const DecodePiece pc = tv.pieces[p];
+      const DecodePiece pc = p == p_begin ? first_piece : tv.pieces[p];
       const int n_all = tv.n[pc.b], n = min(n_all - row0, N);
       if (n <= 0) continue;
       const RingView ring = ring_view(v, pc.b, pc.plen);
