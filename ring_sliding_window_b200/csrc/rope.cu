@@ -133,6 +133,7 @@ __global__ void advance_rope_kernel(const DeviceView v) {
 __global__ void __launch_bounds__(64) tree_rope_kernel(const DeviceView v, const TreeView tv) {
   const int64_t row = blockIdx.x;
   const int b = (int)(row / tv.T), i = (int)(row % tv.T);
+  grid_dependency_wait();
   if (i >= tv.n[b]) return;
   const int half = v.D / 2;
   const int64_t t = v.t[b] + tv.depth[row];
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(64) tree_rope_kernel(const DeviceView v, const
 __global__ void __launch_bounds__(64) tree_advance_kernel(const DeviceView v, int32_t *accepted) {
   const int half = v.D / 2;
   const int b = blockIdx.x;
+  grid_dependency_wait();
   const int64_t t = v.t[b] + accepted[b];
   __syncthreads();  // every thread has read the old counters
   if (threadIdx.x == 0) {
@@ -163,13 +165,11 @@ __global__ void __launch_bounds__(64) tree_advance_kernel(const DeviceView v, in
 
 cudaError_t launch_tree_rope(const DeviceView &v, const TreeView &tv, cudaStream_t s) {
   if (!v.rope) return cudaSuccess;
-  tree_rope_kernel<<<(unsigned)(v.B * tv.T), 64, 0, s>>>(v, tv);
-  return cudaGetLastError();
+  return launch_overlapped(tree_rope_kernel, dim3((unsigned)(v.B * tv.T)), dim3(64), 0, s, v, tv);
 }
 
 cudaError_t launch_tree_advance(const DeviceView &v, int32_t *accepted, cudaStream_t s) {
-  tree_advance_kernel<<<v.B, 64, 0, s>>>(v, accepted);
-  return cudaGetLastError();
+  return launch_overlapped(tree_advance_kernel, dim3((unsigned)v.B), dim3(64), 0, s, v, accepted);
 }
 
 cudaError_t launch_rope_prefill(const DeviceView &v, const void *q, const void *k, void *qr,

@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kCommitThreads)
   const DeviceView &v = a.v;
   const TreeView &tv = a.tv;
   const int b = blockIdx.x, layer = blockIdx.y;
+  grid_dependency_wait();
   int n = a.path_len[b];
   const int drafts = tv.n[b];
   const bool bad_len = n < 0 || n > tv.T;
@@ -580,18 +581,13 @@ rswa_status rswa_tree_commit(rswa_tree *tree, const void *const *k_draft,
     const int64_t z = std::min((chunks + kCommitThreads - 1) / kCommitThreads,
                                std::max<int64_t>(1, 4 * s->num_sms / blocks));
     const dim3 grid((unsigned)s->cfg.batch, (unsigned)n, (unsigned)z);
-    const cudaStream_t st = (cudaStream_t)stream;
-    if (s->cfg.dtype == RSWA_BF16) {
-      if (s->cfg.head_dim == 128)
-        tree_commit_kernel<__nv_bfloat16, 128><<<grid, kCommitThreads, 0, st>>>(a);
-      else
-        tree_commit_kernel<__nv_bfloat16, 64><<<grid, kCommitThreads, 0, st>>>(a);
-    } else if (s->cfg.head_dim == 128) {
-      tree_commit_kernel<float, 128><<<grid, kCommitThreads, 0, st>>>(a);
-    } else {
-      tree_commit_kernel<float, 64><<<grid, kCommitThreads, 0, st>>>(a);
-    }
-    const cudaError_t e = cudaGetLastError();
+    auto *commit = s->cfg.dtype == RSWA_BF16
+                       ? (s->cfg.head_dim == 128 ? tree_commit_kernel<__nv_bfloat16, 128>
+                                                 : tree_commit_kernel<__nv_bfloat16, 64>)
+                       : (s->cfg.head_dim == 128 ? tree_commit_kernel<float, 128>
+                                                 : tree_commit_kernel<float, 64>);
+    const cudaError_t e =
+        launch_overlapped(commit, grid, dim3(kCommitThreads), 0, (cudaStream_t)stream, a);
     if (e != cudaSuccess) return from_cuda(e);
   }
   return RSWA_OK;
