@@ -10,9 +10,8 @@
 // partials that tree_combine_kernel merges.
 //
 // Up to 32 drafts: tree_rows_kernel, 16 of them a CTA.  A warp takes four drafts,
-// their queries and outputs in registers, and four keys at a time, 8 lanes a key;
-// a producer warp streams K and V rows into shared memory by bulk copies.  Every
-// 16 bytes that leave shared memory meet four drafts, in packed FP32 pairs.  Bound
+// their queries and outputs in registers, and four or eight keys at a time, 8 lanes
+// a key; bulk copies stream K and V rows into shared memory.  Every 16 bytes that leave shared memory meet four drafts, in packed FP32 pairs.  Bound
 // by HBM up to 4 drafts (8 x 8,000 tokens, d = 128: 118 us, 87 % of the measured
 // copy rate), by instruction issue from 8 (4 x 4,096 tokens, 16 drafts: 101 us).
 //
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------- up to 32 drafts
-constexpr int kRowWarps = 8;            // consumer warps
+constexpr int kRowWarps = 8;            // (a ninth, for the copies, would cost 80 registers a thread)
 constexpr int kPerWarp = 4;             // drafts of a warp
 constexpr float kGrowth = 8.f;          // m moves past a score 2^8 above it
 
@@ -301,14 +300,21 @@ struct __align__(128) RowsSmem {
   uint64_t full[kStages], empty[kStages];
 };
 
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+
 // G groups of four drafts, 8 / G warps each.
 template <int D, int G>
-__global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
+__global__ void __launch_bounds__(kRowWarps * 32, 1)
     tree_rows_kernel(const TreeSimtArgs a) {
   using Smem = RowsSmem<D>;
   constexpr int NST = Smem::kStages, kRows = Smem::kRows;
   constexpr int kWarps = kRowWarps / G;   // of a group
   constexpr int NP = D / 16;              // pairs of a row's elements on a lane
+  constexpr int kPass = kWarps * 4;       // keys that a group takes at a time
+  constexpr int KK = kRows >= 2 * kPass ? 2 : 1;  // times one or two a lane group
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
   const DeviceView &v = a.v;
@@ -332,33 +338,49 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
     k1 = max(k0, min((pc.key_end - 1) * kKeys, ring.held));
   };
 
-  if (warp == kRowWarps) {
-    // -------------------------------------------------------------- producer
-    // test-only fault injection: no copies at all, so every wait runs out
-    if (lane != 0 || (*v.fault & RSWA_FAULT_DROP_DECODE_COPIES) != 0) return;
-    int it = 0;
-    bool ok = true;
-    for (int p = p_begin; ok && p < p_end; ++p) {
-      const DecodePiece pc = tv.pieces[p];
-      if (tv.n[pc.b] <= row0) continue;
-      const RingView ring = ring_view(v, pc.b, pc.plen);
-      int k0, k1;
-      slots(pc, ring, k0, k1);
-      for (; k0 < k1; k0 += kRows, ++it) {
-        const int s = it % NST;
-        if (!(ok = mbar_wait_bounded(&sm.empty[s], ((it / NST) & 1) ^ 1, v.err, RSWA_DEVERR_TIMEOUT)))
-          break;
-        const uint32_t bytes = (uint32_t)min(kRows, k1 - k0) * (uint32_t)(D * sizeof(float));
-        mbar_arrive_expect_tx(&sm.full[s], 2 * bytes);
-        bulk_g2s(sm.k[s], a.kc + (pc.row0 + k0) * D, bytes, &sm.full[s]);
-        bulk_g2s(sm.v[s], a.vc + (pc.row0 + k0) * D, bytes, &sm.full[s]);
+  // ------------------------------------------------------------------ copies
+  // by warp 0, kStages - 1 ahead of the stage in use
+  struct {
+    int p, k0, k1, it;
+    int64_t row0;
+    bool on;
+  } copy{p_begin, 0, 0, 0, 0, warp == 0};
+  // test-only fault injection: no copies at all, so every wait runs out
+  if ((*v.fault & RSWA_FAULT_DROP_DECODE_COPIES) != 0) copy.on = false;
+  auto copy_next = [&]() {
+    while (copy.on && copy.k0 >= copy.k1) {
+      if (copy.p == p_end) {
+        copy.on = false;
+      } else {
+        const DecodePiece pc = tv.pieces[copy.p++];
+        if (tv.n[pc.b] <= row0) continue;
+        slots(pc, ring_view(v, pc.b, pc.plen), copy.k0, copy.k1);
+        copy.row0 = pc.row0;
       }
     }
-    // every copy issued has landed before the CTA may exit (bounded)
-    for (int s = 0; s < NST && s < it; ++s)
-      mbar_wait_bounded(&sm.full[s], ((it - 1 - s) / NST) & 1, v.err, RSWA_DEVERR_TIMEOUT);
-    return;
-  }
+    if (!copy.on) return;
+    const int s = copy.it % NST;
+    // (a free slot from the second round on: every warp is done with the stage
+    // before the one in use, or soon)
+    const bool free = mbar_wait_bounded(&sm.empty[s], ((copy.it / NST) & 1) ^ 1, v.err,
+                                        RSWA_DEVERR_TIMEOUT);
+    if (!__all_sync(0xffffffffu, free)) {
+      copy.on = false;
+      return;
+    }
+    if (lane == 0) {
+      const uint32_t bytes =
+          (uint32_t)min(kRows, copy.k1 - copy.k0) * (uint32_t)(D * sizeof(float));
+      mbar_arrive_expect_tx(&sm.full[s], 2 * bytes);
+      bulk_g2s(sm.k[s], a.kc + (copy.row0 + copy.k0) * D, bytes, &sm.full[s]);
+      bulk_g2s(sm.v[s], a.vc + (copy.row0 + copy.k0) * D, bytes, &sm.full[s]);
+    }
+    __syncwarp();
+    copy.k0 += kRows;
+    ++copy.it;
+  };
+  if (warp == 0)
+    for (int s = 0; s < NST - 1; ++s) copy_next();
 
   // --------------------------------------------------------------- consumers
   const int li = lane & 7, lg = lane >> 3;       // lane of a key, key of four
@@ -413,8 +435,8 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
         o[r][j] = 0;
       }
     }
-    // one key a lane group: scores, weights, and the value rows that are seen
-    auto score = [&](const uint64_t *k, float *x) {
+    // a lane's part of the scores of one key, and the sums over a key's lanes
+    auto dot = [&](const uint64_t *k, float *x) {
 #pragma unroll
       for (int r = 0; r < kPerWarp; ++r) {
         uint64_t s0 = 0, s1 = 0;
@@ -426,34 +448,41 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
         s0 = tc::fadd2(s0, s1);
         x[r] = tc::f2_lo(s0) + tc::f2_hi(s0);
       }
+    };
+    auto add_lanes = [&](auto count, float *x) {
+      constexpr int N = decltype(count)::value;
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1)
 #pragma unroll
-        for (int r = 0; r < kPerWarp; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], off);
+        for (int e = 0; e < N * kPerWarp; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], off);
     };
-    // seen: bit r, draft r sees the key; `all` if every bit of every lane is set
-    auto weigh = [&](float *x, uint32_t seen, bool all) {
+    // x[4 c + r]: scores of N keys a lane group to weights.  seen: bit 4 c + r, draft
+    // r sees key c; `all` if every bit of every lane is set
+    auto weigh = [&](auto count, float *x, uint32_t seen, bool all) {
+      constexpr int N = decltype(count)::value;
       bool grew = false;
 #pragma unroll
-      for (int r = 0; r < kPerWarp; ++r) {
-        if (!all && !((seen >> r) & 1u)) x[r] = -INFINITY;
-        grew |= x[r] - m[r] > kGrowth;
+      for (int e = 0; e < N * kPerWarp; ++e) {
+        if (!all && !((seen >> e) & 1u)) x[e] = -INFINITY;
+        grew |= x[e] - m[e % kPerWarp] > kGrowth;
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-        for (int r = 0; r < kPerWarp; ++r)
-          if (x[r] - m[r] > kGrowth) {
-            const float f = exp2f(m[r] - x[r]);
-            m[r] = x[r];
+        for (int e = 0; e < N * kPerWarp; ++e) {
+          const int r = e % kPerWarp;
+          if (x[e] - m[r] > kGrowth) {
+            const float f = exp2f(m[r] - x[e]);
+            m[r] = x[e];
             l[r] *= f;
 #pragma unroll
             for (int j = 0; j < NP; ++j) o[r][j] = tc::fmul2(o[r][j], tc::f2_pack(f, f));
           }
+        }
       }
 #pragma unroll
-      for (int r = 0; r < kPerWarp; ++r) {
-        x[r] = exp2f(x[r] - m[r]);
-        l[r] += x[r];
+      for (int e = 0; e < N * kPerWarp; ++e) {
+        x[e] = exp2f(x[e] - m[e % kPerWarp]);
+        l[e % kPerWarp] += x[e];
       }
     };
     auto gather = [&](const uint64_t *val, const float *w, uint32_t seen, bool all) {
@@ -484,8 +513,9 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
         uint64_t row[NP];
         float x[kPerWarp];
         load_row(a.kd + (i * v.H + pc.h) * D, i, true, row);
-        score(row, x);
-        weigh(x, seen, false);
+        dot(row, x);
+        add_lanes(Count<1>(), x);
+        weigh(Count<1>(), x, seen, false);
         load_row(a.vd + (i * v.H + pc.h) * D, i, false, row);
         gather(row, x, seen, false);
       }
@@ -500,26 +530,38 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
       dead = __any_sync(0xffffffffu, dead) != 0;
       if (!dead) {
 #pragma unroll 1
-        for (int r0 = wg * 4; r0 < rows; r0 += kWarps * 4) {
-          const int key = min(r0 + lg, rows - 1);
-          uint32_t seen = 0xfu;
-          if (!all) {
-            const int age = r0 + lg < rows ? slot_age(ring, k0 + key) : INT_MAX;
-            seen = 0;
+        for (int r0 = wg * 4; r0 < rows; r0 += KK * kPass) {
+          int key[KK];
+          uint32_t seen = 0;
+          float x[KK * kPerWarp];
 #pragma unroll
-            for (int r = 0; r < kPerWarp; ++r) seen |= (age <= limit[r] ? 1u : 0u) << r;
+          for (int c = 0; c < KK; ++c) {
+            const int at = r0 + c * kPass + lg;
+            key[c] = min(at, rows - 1);
+            if (!all) {
+              const int age = at < rows ? slot_age(ring, k0 + at) : INT_MAX;
+#pragma unroll
+              for (int r = 0; r < kPerWarp; ++r)
+                seen |= (age <= limit[r] ? 1u : 0u) << (c * kPerWarp + r);
+            }
           }
-          uint64_t row[NP];
-          float x[kPerWarp];
-          from_smem(sm.k[s] + key * D, row);
-          score(row, x);
-          weigh(x, seen, all);
-          from_smem(sm.v[s] + key * D, row);
-          gather(row, x, seen, all);
+          uint64_t row[KK][NP];
+#pragma unroll
+          for (int c = 0; c < KK; ++c) from_smem(sm.k[s] + key[c] * D, row[c]);
+#pragma unroll
+          for (int c = 0; c < KK; ++c) dot(row[c], x + c * kPerWarp);
+          add_lanes(Count<KK>(), x);
+#pragma unroll
+          for (int c = 0; c < KK; ++c) from_smem(sm.v[s] + key[c] * D, row[c]);
+          weigh(Count<KK>(), x, seen, all);
+#pragma unroll
+          for (int c = 0; c < KK; ++c)
+            gather(row[c], x + c * kPerWarp, seen >> (c * kPerWarp), all);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[s]);
+      if (warp == 0) copy_next();
     }
 
     // the warp's four lane groups, then the group's warps
@@ -581,6 +623,9 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1)
     __syncwarp();
     named_bar_sync(1, kRowWarps * 32);  // the partials are read
   }
+  // every copy issued has landed before the CTA may exit (bounded)
+  for (int s = 0; s < NST && s < copy.it; ++s)
+    mbar_wait_bounded(&sm.full[s], ((copy.it - 1 - s) / NST) & 1, v.err, RSWA_DEVERR_TIMEOUT);
 }
 
 template <typename Smem>
@@ -594,7 +639,7 @@ cudaError_t launch_rows(const TreeSimtArgs &a, cudaStream_t s) {
   cudaError_t e = prepare_kernel<RowsSmem<D>>(tree_rows_kernel<D, G>);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + kRowsCta - 1) / kRowsCta));
-  return launch_overlapped(tree_rows_kernel<D, G>, grid, dim3((kRowWarps + 1) * 32),
+  return launch_overlapped(tree_rows_kernel<D, G>, grid, dim3(kRowWarps * 32),
                            sizeof(RowsSmem<D>), s, a);
 }
 
