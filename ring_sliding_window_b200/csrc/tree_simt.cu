@@ -10,16 +10,18 @@
 // partials that tree_combine_kernel merges.
 //
 // Up to 32 drafts: tree_rows_kernel, 16 of them a CTA.  A warp takes four drafts,
-// their queries and outputs in registers, and four or eight keys at a time, 8 lanes
-// a key; bulk copies stream K and V rows into shared memory.  Every 16 bytes that leave shared memory meet four drafts, in packed FP32 pairs.  Bound
-// by HBM up to 4 drafts (8 x 8,000 tokens, d = 128: 118 us, 87 % of the measured
-// copy rate), by instruction issue from 8 (4 x 4,096 tokens, 16 drafts: 101 us).
+// their queries and outputs in registers, and four to sixteen keys at a time, d / 16
+// lanes a key; bulk copies stream K and V rows into shared memory.  Every 16 bytes
+// that leave shared memory meet four drafts, in packed FP32 pairs.  Bound by HBM up
+// to 4 drafts (8 x 8,000 tokens, d = 128: 122 us, 84 % of the measured copy rate),
+// by the latency of a key's chain (products, shuffles, exponential, products) with
+// two warps a scheduler from 8 (4 x 4,096 tokens: 84 us for 16 drafts).
 //
 // More: tree_simt_kernel, row groups of 64.  A tile is 64 keys: 256 threads form
 // a 16 x 16 grid, each with 4 query rows x 4 keys of the scores, then the same
 // rows x D / 16 output columns.  Bound by FP32 FMA issue and the barriers between
-// its phases (4 x 4,096 tokens: 32 drafts would take 235 us for the rows
-// kernel's 186, 64 take 239 for its 373).
+// its phases.  4 x 4,096 tokens: 235 us for 33 to 64 drafts, where the rows kernel
+// takes 156 for 32 and 373 for 64.
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
@@ -312,8 +314,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   using Smem = RowsSmem<D>;
   constexpr int NST = Smem::kStages, kRows = Smem::kRows;
   constexpr int kWarps = kRowWarps / G;   // of a group
-  constexpr int NP = D / 16;              // pairs of a row's elements on a lane
-  constexpr int kPass = kWarps * 4;       // keys that a group takes at a time
+  constexpr int LK = D / 16, KG = 32 / LK;  // lanes of a key, keys of a warp
+  constexpr int NP = 8;                   // pairs of a row's elements on a lane (4 chunks)
+  constexpr int kPass = kWarps * KG;      // keys that a group takes at a time
   constexpr int KK = kRows >= 2 * kPass ? 2 : 1;  // times one or two a lane group
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -383,7 +386,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     for (int s = 0; s < NST - 1; ++s) copy_next();
 
   // --------------------------------------------------------------- consumers
-  const int li = lane & 7, lg = lane >> 3;       // lane of a key, key of four
+  const int li = lane % LK, lg = lane / LK;      // lane of a key, key of the warp's
+  // 16-byte chunk j of a lane's four.  Two keys of d = 64 share a quarter warp's
+  // load: the odd one takes the chunks in another order, so the banks differ.
+  auto chunk = [&](int j) { return li + LK * (D == 64 ? j ^ (lg & 1) : j); };
   const int group = warp / kWarps, wg = warp % kWarps;
   const float qs = v.scale * kLog2e;
   int it = 0;
@@ -394,24 +400,23 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     if (n <= row0) continue;
     const RingView ring = ring_view(v, pc.b, pc.plen);
     const int64_t draft0 = (int64_t)pc.b * tv.T;
-    // a row's chunks li, li + 8, ... (16 bytes each) as packed pairs, turned at
-    // draft i's position if RoPE is on
+    // a lane's part of a row as packed pairs, turned at draft i's position if RoPE is on
     auto load_row = [&](const float *src, int64_t i, bool turn, uint64_t *x) {
       float f[2 * NP];
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j)
+      for (int j = 0; j < 4; ++j)
         *reinterpret_cast<float4 *>(f + 4 * j) =
-            *reinterpret_cast<const float4 *>(src + (li + 8 * j) * 4);
+            *reinterpret_cast<const float4 *>(src + chunk(j) * 4);
       if (turn && v.rope) {
         const float2 *cs = tv.cs + i * (D / 2);
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 w = cs[(li + 8 * j) * 4 + e];
-            const float c0 = f[4 * j + e], c1 = f[4 * (j + D / 64) + e];
+            const float2 w = cs[chunk(j) * 4 + e];
+            const float c0 = f[4 * j + e], c1 = f[4 * (j + 2) + e];
             f[4 * j + e] = c0 * w.x - c1 * w.y;
-            f[4 * (j + D / 64) + e] = c1 * w.x + c0 * w.y;
+            f[4 * (j + 2) + e] = c1 * w.x + c0 * w.y;
           }
       }
 #pragma unroll
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     auto add_lanes = [&](auto count, float *x) {
       constexpr int N = decltype(count)::value;
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1)
+      for (int off = 1; off < LK; off <<= 1)
 #pragma unroll
         for (int e = 0; e < N * kPerWarp; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], off);
     };
@@ -495,15 +500,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     };
     auto from_smem = [&](const float *row, uint64_t *x) {
 #pragma unroll
-      for (int j = 0; j < NP; j += 2) {
-        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row + (li + 4 * j) * 4);
-        x[j] = u.x;
-        x[j + 1] = u.y;
+      for (int j = 0; j < 4; ++j) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row + chunk(j) * 4);
+        x[2 * j] = u.x;
+        x[2 * j + 1] = u.y;
       }
     };
 
     if (pc.key_begin == 0) {
-      for (int j0 = wg * 4; j0 < n; j0 += kWarps * 4) {
+      for (int j0 = wg * KG; j0 < n; j0 += kPass) {
         const int key = j0 + lg;
         const int64_t i = draft0 + min(key, n - 1);
         uint32_t seen = 0;
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       dead = __any_sync(0xffffffffu, dead) != 0;
       if (!dead) {
 #pragma unroll 1
-        for (int r0 = wg * 4; r0 < rows; r0 += KK * kPass) {
+        for (int r0 = wg * KG; r0 < rows; r0 += KK * kPass) {
           int key[KK];
           uint32_t seen = 0;
           float x[KK * kPerWarp];
@@ -564,15 +569,25 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       if (warp == 0) copy_next();
     }
 
-    // the warp's four lane groups, then the group's warps
+    // the warp's lane groups, then the group's warps
 #pragma unroll
     for (int r = 0; r < kPerWarp; ++r) {
-      const float top = fmaxf(fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 8)),
-                              __shfl_xor_sync(0xffffffffu, fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 8)), 16));
+      if (D == 64 && (lg & 1))
+#pragma unroll
+        for (int j = 0; j < NP; j += 4)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t x = o[r][j + e];
+            o[r][j + e] = o[r][j + 2 + e];
+            o[r][j + 2 + e] = x;
+          }
+      float top = m[r];
+#pragma unroll
+      for (int off = LK; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
       const float f = exp2f(m[r] - top);
       float lr = l[r] * f;
-      lr += __shfl_xor_sync(0xffffffffu, lr, 8);
-      lr += __shfl_xor_sync(0xffffffffu, lr, 16);
+#pragma unroll
+      for (int off = LK; off < 32; off <<= 1) lr += __shfl_xor_sync(0xffffffffu, lr, off);
       if (lane == 0) {
         sm.red_m[warp][r] = top;
         sm.red_l[warp][r] = lr;
@@ -580,12 +595,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         float x = tc::f2_lo(o[r][j]) * f, y = tc::f2_hi(o[r][j]) * f;
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        y += __shfl_xor_sync(0xffffffffu, y, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        y += __shfl_xor_sync(0xffffffffu, y, 16);
+#pragma unroll
+        for (int off = LK; off < 32; off <<= 1) {
+          x += __shfl_xor_sync(0xffffffffu, x, off);
+          y += __shfl_xor_sync(0xffffffffu, y, off);
+        }
         if (lg == 0)
-          *reinterpret_cast<float2 *>(&sm.red_o[warp][r][(li + 8 * (j >> 1)) * 4 + (j & 1) * 2]) =
+          *reinterpret_cast<float2 *>(&sm.red_o[warp][r][(li + LK * (j >> 1)) * 4 + (j & 1) * 2]) =
               make_float2(x, y);
       }
     }
