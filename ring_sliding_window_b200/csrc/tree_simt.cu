@@ -20,8 +20,8 @@
 // More: tree_simt_kernel, row groups of 64.  A tile is 64 keys: 256 threads form
 // a 16 x 16 grid, each with 4 query rows x 4 keys of the scores, then the same
 // rows x D / 16 output columns.  Bound by FP32 FMA issue and the barriers between
-// its phases.  4 x 4,096 tokens: 235 us for 33 to 64 drafts, where the rows kernel
-// takes 156 for 32 and 373 for 64.
+// its phases.  4 x 4,096 tokens: 188 us for 33 to 64 drafts, where the rows kernel
+// takes 157 for 32 and twice that for 64.
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
@@ -39,14 +39,17 @@ constexpr int kKeys = kTreeSimtTile;
 constexpr int kThreads = 256;
 constexpr int kRowsMax = 32;      // drafts that tree_rows_kernel takes
 constexpr int kRowsCta = 16;      // of them a CTA
-constexpr float kMasked = -1.f;  // marks an unseen pair where a weight (>= 0) would stand
 
 template <int D>
 struct SimtSmem {
   static constexpr int kRows = 64;
   float q[kRows][D + 4];
+  // d = 128: one buffer, a tile's K until its scores are done, then its V, so that
+  // two CTAs fit an SM (205 us for 235 at 4 x 64 drafts over 4,096 tokens)
+  static constexpr bool kShared = D == 128;
   float k[kKeys][D + 4];
-  float v[kKeys][D + 4];
+  float v_own[kShared ? 1 : kKeys][D + 4];
+  __device__ float (*v())[D + 4] { return kShared ? k : v_own; }
   float p[kRows][kKeys + 4];
   float alpha[kRows];
   int limit[kRows];     // W - 1 - depth of the row
@@ -59,6 +62,11 @@ struct TreeSimtArgs {
   TreeView tv;
   const float *q, *kd, *vd, *kc, *vc;
   float *out;
+};
+
+template <int N>
+struct Count {
+  static constexpr int value = N;
 };
 
 // Elements 4 c .. 4 c + 3 of both halves of the row at `src` into dst, turned by
@@ -85,8 +93,9 @@ __device__ __forceinline__ void load_rotated(const float *src, float *dst, int c
   *reinterpret_cast<float4 *>(dst + c * N + D / 2) = make_float4(b[0], b[1], b[2], b[3]);
 }
 
+// Two CTAs an SM: one's loads and softmax behind the other's products.
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     tree_simt_kernel(const TreeSimtArgs a) {
   using Smem = SimtSmem<D>;
   constexpr int kRows = Smem::kRows;
@@ -124,11 +133,11 @@ __global__ void __launch_bounds__(kThreads)
       sm.above[r] = tv.above[i];
     }
     float m = -INFINITY, l = 0.f;  // of row tid / kTPR
-    float acc[kRT][kCT * 4];
+    uint64_t acc[kRT][kCT * 2];  // columns in pairs
 #pragma unroll
     for (int i = 0; i < kRT; ++i)
 #pragma unroll
-      for (int c = 0; c < kCT * 4; ++c) acc[i][c] = 0.f;
+      for (int c = 0; c < kCT * 2; ++c) acc[i][c] = 0;
 
     for (int tl = pc.key_begin; tl < pc.key_end; ++tl) {
       const bool drafts = tl < n_draft_tiles;
@@ -141,15 +150,39 @@ __global__ void __launch_bounds__(kThreads)
         if (r >= nk) continue;  // masked below, its contents unused
         if (drafts) {
           const int64_t i = draft0 + k0 + r;
-          const int64_t off = (i * v.H + pc.h) * D;
-          load_rotated<D>(a.kd + off, sm.k[r], c,
-                             v.rope ? tv.cs + i * (D / 2) : nullptr);
-          load_rotated<D>(a.vd + off, sm.v[r], c, nullptr);
+          load_rotated<D>(a.kd + (i * v.H + pc.h) * D, sm.k[r], c,
+                          v.rope ? tv.cs + i * (D / 2) : nullptr);
         } else {
-          const int64_t off = (pc.row0 + k0 + r) * D;
-          load_rotated<D>(a.kc + off, sm.k[r], c, nullptr);
-          load_rotated<D>(a.vc + off, sm.v[r], c, nullptr);
+          load_rotated<D>(a.kc + (pc.row0 + k0 + r) * D, sm.k[r], c, nullptr);
         }
+      }
+      // V: from memory to registers, and from there to shared memory (0 behind the
+      // last entry)
+      constexpr int kLoads = kKeys * (D / N) / kThreads;
+      float4 vreg[kLoads];
+      bool bad = false;  // a value that is not finite
+      auto fetch_v = [&]() {
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int at = tid + e * kThreads, r = at / (D / N), c = at % (D / N) * N;
+          vreg[e] = r >= nk ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : *reinterpret_cast<const float4 *>(
+                                  drafts ? a.vd + ((draft0 + k0 + r) * v.H + pc.h) * D + c
+                                         : a.vc + (pc.row0 + k0 + r) * D + c);
+        }
+      };
+      auto store_v = [&]() {
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int at = tid + e * kThreads, r = at / (D / N), c = at % (D / N) * N;
+          const float4 x = vreg[e];
+          bad |= !isfinite(x.x) || !isfinite(x.y) || !isfinite(x.z) || !isfinite(x.w);
+          *reinterpret_cast<float4 *>(&sm.v()[r][c]) = x;
+        }
+      };
+      if constexpr (!Smem::kShared) {
+        fetch_v();
+        store_v();
       }
       if (!drafts && tid < kKeys) sm.age[tid] = slot_age(ring, k0 + tid);
       __syncthreads();
@@ -181,6 +214,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sm.p[ty + 16 * i][tx + 16 * j] = s[i][j] * qs;
       __syncthreads();
+      if constexpr (Smem::kShared) fetch_v();  // behind the softmax
       {
         // softmax of row r by kTPR neighbouring threads
         const int r = tid / kTPR, sub = tid % kTPR;
@@ -210,8 +244,8 @@ __global__ void __launch_bounds__(kThreads)
         float lt = 0.f;
 #pragma unroll
         for (int j = 0; j < kKeys / kTPR; ++j) {
-          const float w = see[j] ? exp2f(x[j] - sub_m) : kMasked;
-          if (see[j]) lt += w;
+          const float w = see[j] ? exp2f(x[j] - sub_m) : 0.f;
+          lt += w;
           sm.p[r][sub + kTPR * j] = w;
         }
 #pragma unroll
@@ -220,40 +254,55 @@ __global__ void __launch_bounds__(kThreads)
         m = m_new;
         if (sub == 0) sm.alpha[r] = corr;
       }
-      __syncthreads();
+      if constexpr (Smem::kShared) store_v();
+      bad = __syncthreads_or(bad) != 0;
 #pragma unroll
       for (int i = 0; i < kRT; ++i) {
         const float corr = sm.alpha[ty + 16 * i];
 #pragma unroll
-        for (int c = 0; c < kCT * 4; ++c) acc[i][c] *= corr;
+        for (int c = 0; c < kCT * 2; ++c) acc[i][c] = tc::fmul2(acc[i][c], tc::f2_pack(corr, corr));
       }
+      auto sees = [&](int row, int key) {
+        if (!drafts) return key < nk && sm.age[key] <= sm.limit[row];
+        const uint4 ab = sm.above[row];
+        const int node = k0 + key, w = node >> 5;
+        return key < nk &&
+               (((w == 0 ? ab.x : w == 1 ? ab.y : w == 2 ? ab.z : ab.w) >> (node & 31)) & 1u) != 0u;
+      };
+      auto products = [&](auto check) {
 #pragma unroll 2
-      for (int j0 = 0; j0 < nk; j0 += 4) {  // (rows of V behind the last entry have w < 0)
-        float4 w4[kRT];
+        for (int j0 = 0; j0 < nk; j0 += 4) {
+          float4 w4[kRT];
 #pragma unroll
-        for (int i = 0; i < kRT; ++i)
-          w4[i] = *reinterpret_cast<const float4 *>(&sm.p[ty + 16 * i][j0]);
+          for (int i = 0; i < kRT; ++i)
+            w4[i] = *reinterpret_cast<const float4 *>(&sm.p[ty + 16 * i][j0]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float4 vv[kCT];
+          for (int u = 0; u < 4; ++u) {
+            ulonglong2 vv[kCT];
 #pragma unroll
-          for (int c = 0; c < kCT; ++c)
-            vv[c] = *reinterpret_cast<const float4 *>(&sm.v[j0 + u][tx * 4 + 64 * c]);
+            for (int c = 0; c < kCT; ++c)
+              vv[c] = *reinterpret_cast<const ulonglong2 *>(&sm.v()[j0 + u][tx * 4 + 64 * c]);
 #pragma unroll
-          for (int i = 0; i < kRT; ++i) {
-            const float w = u == 0 ? w4[i].x : u == 1 ? w4[i].y : u == 2 ? w4[i].z : w4[i].w;
-            if (w >= 0.f || w != w) {  // an unseen entry's value never enters, whatever it holds
+            for (int i = 0; i < kRT; ++i) {
+              const float w = u == 0 ? w4[i].x : u == 1 ? w4[i].y : u == 2 ? w4[i].z : w4[i].w;
+              if (!decltype(check)::value || sees(ty + 16 * i, j0 + u)) {
+                const uint64_t w2 = tc::f2_pack(w, w);
 #pragma unroll
-              for (int c = 0; c < kCT; ++c) {
-                acc[i][4 * c] = fmaf(w, vv[c].x, acc[i][4 * c]);
-                acc[i][4 * c + 1] = fmaf(w, vv[c].y, acc[i][4 * c + 1]);
-                acc[i][4 * c + 2] = fmaf(w, vv[c].z, acc[i][4 * c + 2]);
-                acc[i][4 * c + 3] = fmaf(w, vv[c].w, acc[i][4 * c + 3]);
+                for (int c = 0; c < kCT; ++c) {
+                  acc[i][2 * c] = tc::ffma2(w2, vv[c].x, acc[i][2 * c]);
+                  acc[i][2 * c + 1] = tc::ffma2(w2, vv[c].y, acc[i][2 * c + 1]);
+                }
               }
             }
           }
         }
-      }
+      };
+      // an unseen entry's weight is 0; where its value would make 0 x inf of that it
+      // is left out one by one
+      if (!bad)
+        products(Count<0>());
+      else
+        products(Count<1>());
     }
 
     // the piece's result: final where it is the ring's only one, else a partial
@@ -273,14 +322,14 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int c = 0; c < kCT; ++c) {
         const int e = tx * 4 + 64 * c;
+        float4 x = make_float4(tc::f2_lo(acc[i][2 * c]), tc::f2_hi(acc[i][2 * c]),
+                               tc::f2_lo(acc[i][2 * c + 1]), tc::f2_hi(acc[i][2 * c + 1]));
         if (pc.count == 1) {
           const float sum = sm.alpha[ty + 16 * i];
-          float *dst = a.out + ((draft0 + r) * v.H + pc.h) * D + e;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) dst[x] = acc[i][4 * c + x] / sum;
+          x = make_float4(x.x / sum, x.y / sum, x.z / sum, x.w / sum);
+          *reinterpret_cast<float4 *>(a.out + ((draft0 + r) * v.H + pc.h) * D + e) = x;
         } else {
-          *reinterpret_cast<float4 *>(tv.part_o + ((int64_t)p * tv.T + r) * D + e) =
-              make_float4(acc[i][4 * c], acc[i][4 * c + 1], acc[i][4 * c + 2], acc[i][4 * c + 3]);
+          *reinterpret_cast<float4 *>(tv.part_o + ((int64_t)p * tv.T + r) * D + e) = x;
         }
       }
     }
@@ -300,11 +349,6 @@ struct __align__(128) RowsSmem {
   float red_o[kRowWarps][kPerWarp][D];
   float red_m[kRowWarps][kPerWarp], red_l[kRowWarps][kPerWarp];
   uint64_t full[kStages], empty[kStages];
-};
-
-template <int N>
-struct Count {
-  static constexpr int value = N;
 };
 
 // G groups of four drafts, 8 / G warps each.
