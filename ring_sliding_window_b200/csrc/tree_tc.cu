@@ -10,11 +10,11 @@
 // else behind them.
 //
 // The 128-key tiles of all rings (a ring's drafts first, then its cache) are
-// cut into one equal range per CTA, one CTA an SM; a ring in several pieces
-// leaves partials that tree_combine_kernel merges.  Inside a CTA:
+// cut into one range of about equal cost per CTA, one CTA an SM; a ring in several
+// pieces leaves partials that tree_combine_kernel merges.  Inside a CTA:
 //   producer warp   K and V tiles by TMA (128-byte swizzle) into two rings of
-//                   kStages slots, and the N query rows of each piece;
-//   MMA warp        one thread: S^T = K Q^T (128 keys x N drafts) into one of
+//                   slots, and the N query rows of each piece;
+//   MMA warp        an elected lane: S^T = K Q^T (128 keys x N drafts) into one of
 //                   two TMEM buffers, a tile ahead of O^T += V^T P;
 //   softmax warps   thread r of four warps owns key r of the tile (TMEM lane r)
 //                   and 16 drafts (32 for N = 64): 4, 8 or 8 warps;
@@ -24,7 +24,7 @@
 // With the keys on the lanes the work of a tile grows with the drafts (N = 16,
 // 32 or 64), and all lanes take part however few they are.  What a softmax needs
 // across the lanes is kept off the ordinary tile: the subtracted m_i only moves
-// when a score exceeds it by more than 2^8, which one barrier with an OR finds
+// when a score exceeds it by more than 2^16, which one barrier with an OR finds
 // out, and the sums over the keys stay per lane until a piece ends.
 //
 // More than 64 drafts are two columns of the grid with N = 64: half the SMs
@@ -62,7 +62,9 @@ namespace {
 
 constexpr int kTile = kTreeTcTile;          // keys per tile
 constexpr int kHalfBytes = kTile * 64 * 2;  // one 64-column swizzled block: 16 KB
-constexpr float kGrowth = 8.0f;             // log2 units
+// Log2 units.  Weights of up to 2^16 are no less precise: FP32 sums and bf16 pairs
+// keep their relative error, and what underflows lies 2^-126 below the weight 1.
+constexpr float kGrowth = 16.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int N>
@@ -96,8 +98,8 @@ struct __align__(1024) TreeSmem {
   float neg_m[N];      // -m of every draft
   float alpha[N];      // factors of a growth
   int top[N];          // largest scores of a tile, as ordered_int (INT_MIN between growths)
-  float sums[2][4][N]; // a finished piece's sums, a warp's lanes each, and its m
-  float m[2][N];
+  float sums[2][4][N]; // a finished piece's sums over each warp's keys
+  float m[2][N];       // and its m
   float inv[N];        // side warps: 1 / sum
   __align__(4) uint8_t depth[N];
   uint64_t q_full[S::kQBufs], q_free[S::kQBufs];
