@@ -20,7 +20,7 @@
 // More: tree_simt_kernel, row groups of 64.  A tile is 64 keys: 256 threads form
 // a 16 x 16 grid, each with 4 query rows x 4 keys of the scores, then the same
 // rows x D / 16 output columns.  Bound by FP32 FMA issue and the barriers between
-// its phases.  4 x 4,096 tokens: 188 us for 33 to 64 drafts, where the rows kernel
+// its phases.  4 x 4,096 tokens: 184 us for 33 to 64 drafts, where the rows kernel
 // takes 157 for 32 and twice that for 64.
 #include <cuda_runtime.h>
 #include <float.h>
@@ -62,6 +62,7 @@ struct TreeSimtArgs {
   TreeView tv;
   const float *q, *kd, *vd, *kc, *vc;
   float *out;
+  int row_base;  // rows kernel: the first draft of its grid's first row
 };
 
 template <int N>
@@ -192,23 +193,34 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < kRT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      auto scores = [&](auto count) {  // of the first 16 J keys
+        constexpr int J = decltype(count)::value;
 #pragma unroll 4
-      for (int c = 0; c < D; c += 4) {
-        float4 qv[kRT], kv[4];
+        for (int c = 0; c < D; c += 4) {
+          float4 qv[kRT], kv[J];
 #pragma unroll
-        for (int i = 0; i < kRT; ++i) qv[i] = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][c]);
+          for (int i = 0; i < kRT; ++i)
+            qv[i] = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][c]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][c]);
+          for (int j = 0; j < J; ++j)
+            kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][c]);
 #pragma unroll
-        for (int i = 0; i < kRT; ++i)
+          for (int i = 0; i < kRT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-            s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-            s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-            s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
-          }
-      }
+            for (int j = 0; j < J; ++j) {
+              s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+              s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+              s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+              s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+            }
+        }
+      };
+      if (nk <= 16)
+        scores(Count<1>());
+      else if (nk <= 32)
+        scores(Count<2>());
+      else
+        scores(Count<4>());
 #pragma unroll
       for (int i = 0; i < kRT; ++i)
 #pragma unroll
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   const DeviceView &v = a.v;
   const TreeView &tv = a.tv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = (int)blockIdx.y * kRowsCta;  // this CTA's first draft
+  const int row0 = a.row_base + (int)blockIdx.y * kRowsCta;  // this CTA's first draft
   const int p_begin = tv.cta_piece[blockIdx.x], p_end = tv.cta_piece[blockIdx.x + 1];
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
@@ -469,13 +481,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     uint64_t q[kPerWarp][NP], o[kPerWarp][NP];
     float m[kPerWarp], l[kPerWarp];
     int limit[kPerWarp];
-    uint32_t above[kPerWarp];  // (32 drafts at most)
 #pragma unroll
     for (int r = 0; r < kPerWarp; ++r) {
       const int64_t i = draft0 + min(row0 + group * kPerWarp + r, n - 1);
       load_row(a.q + (i * v.H + pc.h) * D, i, true, q[r]);
       limit[r] = v.W - 1 - tv.depth[i];
-      above[r] = tv.above[i].x;
       m[r] = -FLT_MAX;
       l[r] = 0.f;
 #pragma unroll
@@ -558,7 +568,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         uint32_t seen = 0;
 #pragma unroll
         for (int r = 0; r < kPerWarp; ++r)
-          seen |= (key < n && ((above[r] >> key) & 1u) ? 1u : 0u) << r;
+          if (key < n) {
+            const int64_t q_row = draft0 + min(row0 + group * kPerWarp + r, n - 1);
+            const uint32_t above = reinterpret_cast<const uint32_t *>(tv.above + q_row)[key >> 5];
+            seen |= ((above >> (key & 31)) & 1u) << r;
+          }
         uint64_t row[NP];
         float x[kPerWarp];
         load_row(a.kd + (i * v.H + pc.h) * D, i, true, row);
@@ -695,24 +709,33 @@ cudaError_t prepare_kernel(void (*kernel)(TreeSimtArgs)) {
 }
 
 template <int D, int G>
-cudaError_t launch_rows(const TreeSimtArgs &a, cudaStream_t s) {
+cudaError_t launch_rows(const TreeSimtArgs &a, int rows, cudaStream_t s) {
   cudaError_t e = prepare_kernel<RowsSmem<D>>(tree_rows_kernel<D, G>);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + kRowsCta - 1) / kRowsCta));
+  const dim3 grid((unsigned)a.tv.grid, (unsigned)((rows + kRowsCta - 1) / kRowsCta));
   return launch_overlapped(tree_rows_kernel<D, G>, grid, dim3(kRowWarps * 32),
                            sizeof(RowsSmem<D>), s, a);
 }
 
+// Whole groups of 64 drafts, and a rest of more than kRowsMax, by the tiled
+// kernel; a smaller rest by the rows kernel (65 drafts as 64 + 1, not as 128).
 template <int D>
-cudaError_t launch_d(const TreeSimtArgs &a, cudaStream_t s) {
-  if (a.tv.T <= 4) return launch_rows<D, 1>(a, s);
-  if (a.tv.T <= 8) return launch_rows<D, 2>(a, s);
-  if (a.tv.T <= kRowsMax) return launch_rows<D, 4>(a, s);
-  cudaError_t e = prepare_kernel<SimtSmem<D>>(tree_simt_kernel<D>);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_d(TreeSimtArgs a, cudaStream_t s) {
   constexpr int kRows = SimtSmem<D>::kRows;
-  const dim3 grid((unsigned)a.tv.grid, (unsigned)((a.tv.T + kRows - 1) / kRows));
-  return launch_overlapped(tree_simt_kernel<D>, grid, dim3(kThreads), sizeof(SimtSmem<D>), s, a);
+  const int rest = a.tv.T % kRows;
+  const bool split = rest > 0 && rest <= kRowsMax;
+  const int groups = a.tv.T / kRows + (rest > 0 && !split ? 1 : 0);
+  if (groups > 0) {
+    cudaError_t e = prepare_kernel<SimtSmem<D>>(tree_simt_kernel<D>);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)a.tv.grid, (unsigned)groups);
+    e = launch_overlapped(tree_simt_kernel<D>, grid, dim3(kThreads), sizeof(SimtSmem<D>), s, a);
+    if (e != cudaSuccess || !split) return e;
+  }
+  a.row_base = a.tv.T / kRows * kRows;
+  if (rest <= 4) return launch_rows<D, 1>(a, rest, s);
+  if (rest <= 8) return launch_rows<D, 2>(a, rest, s);
+  return launch_rows<D, 4>(a, rest, s);
 }
 
 template <int D>
@@ -737,7 +760,7 @@ int tree_simt_ctas(int num_sms, int head_dim, int T) {
 cudaError_t launch_tree_simt(const DeviceView &v, const TreeView &tv, const float *q,
                              const float *kd, const float *vd, const float *kc, const float *vc,
                              float *out, cudaStream_t s) {
-  const TreeSimtArgs a{v, tv, q, kd, vd, kc, vc, out};
+  const TreeSimtArgs a{v, tv, q, kd, vd, kc, vc, out, 0};
   return v.D == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
 }
 

@@ -338,6 +338,24 @@ def test_wide_trees(dtype, d, swa):
 
 
 @pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("T", [68, 72, 80, 96, 127])
+def test_trees_a_little_wider_than_a_group(dtype, d, T):
+    """A few rows past 64 drafts, chains among them, values and keys unseen by some not finite."""
+    rng = np.random.default_rng(T)
+    n = (T, 66, 64, 3)
+    parents = [[i - 1 for i in range(T)]] + [ref.random_parents(rng, T, reach=50) for _ in n[1:]]
+    c = Case(dtype, d, 2, 100, (61, 189, 0, 130), (100, 7, 300, 0), T, n=n, parents=parents)
+    rows = (0, 1, 15, 16, 31, 62, 63, 64, 65, 66, 67, 70, 71, 79, 80, 95, 126)
+    clean = c.run()
+    c.check(clean, rows=rows)
+    # the last drafts of the first sequence: seen by themselves and each other alone
+    c.k[0, T - 2:, :, 1] = float("inf")
+    c.v[0, T - 2:, :, 2] = -float("inf")
+    out = c.run()
+    assert torch.equal(out[0, :T - 2], clean[0, :T - 2]) and torch.equal(out[1:], clean[1:])
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
 @pytest.mark.parametrize("rope", [1, 2])
 def test_wide_trees_turn_with_rope(dtype, d, rope):
     """Every node of a 100-node tree under RoPE gives what a tree of its path alone gives."""
