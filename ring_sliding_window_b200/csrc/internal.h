@@ -64,7 +64,7 @@ constexpr int kTopkMaxVocab = 16 * 16384;    // 16 CTAs of 16,384 columns per ro
 constexpr int kTopkMaxWindow = 8192;         // history staged in shared memory
 constexpr int kTreeTcTile = 128;    // keys per tile of the tensor-core tree kernel
 constexpr int kTreeTcRows = 64;     // drafts that a CTA of it takes
-constexpr int kTreeTcPieceCost = 2; // tiles that a piece's beginning and end cost
+constexpr int kTreeTcPieceCost = 1; // tiles that a piece's beginning and end cost
 constexpr int kTreeSimtTile = 64;   // keys per tile of the FP32 tree kernels
 constexpr int kTreeSimtPieceCost = 1;
 constexpr int kPrefillTile = 128;  // query rows per prefill tile (tensor-core kernel)

@@ -702,15 +702,20 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     mbar_wait_bounded(&sm.full[s], ((copy.it - 1 - s) / NST) & 1, v.err, RSWA_DEVERR_TIMEOUT);
 }
 
-template <typename Smem>
-cudaError_t prepare_kernel(void (*kernel)(TreeSimtArgs)) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sizeof(Smem));
+template <typename Smem, void (*kKernel)(TreeSimtArgs)>
+cudaError_t prepare_kernel() {
+  static bool attr_set[64] = {};  // per device
+  const int dev = current_device();
+  if (dev >= 0 && dev < 64 && attr_set[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(
+      kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+  if (e == cudaSuccess && dev >= 0 && dev < 64) attr_set[dev] = true;
+  return e;
 }
 
 template <int D, int G>
 cudaError_t launch_rows(const TreeSimtArgs &a, int rows, cudaStream_t s) {
-  cudaError_t e = prepare_kernel<RowsSmem<D>>(tree_rows_kernel<D, G>);
+  cudaError_t e = prepare_kernel<RowsSmem<D>, tree_rows_kernel<D, G>>();
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.tv.grid, (unsigned)((rows + kRowsCta - 1) / kRowsCta));
   return launch_overlapped(tree_rows_kernel<D, G>, grid, dim3(kRowWarps * 32),
@@ -726,7 +731,7 @@ cudaError_t launch_d(TreeSimtArgs a, cudaStream_t s) {
   const bool split = rest > 0 && rest <= kRowsMax;
   const int groups = a.tv.T / kRows + (rest > 0 && !split ? 1 : 0);
   if (groups > 0) {
-    cudaError_t e = prepare_kernel<SimtSmem<D>>(tree_simt_kernel<D>);
+    cudaError_t e = prepare_kernel<SimtSmem<D>, tree_simt_kernel<D>>();
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)a.tv.grid, (unsigned)groups);
     e = launch_overlapped(tree_simt_kernel<D>, grid, dim3(kThreads), sizeof(SimtSmem<D>), s, a);
@@ -741,7 +746,7 @@ cudaError_t launch_d(TreeSimtArgs a, cudaStream_t s) {
 template <int D>
 int ctas_d() {
   int n = 0;
-  if (prepare_kernel<SimtSmem<D>>(tree_simt_kernel<D>) != cudaSuccess ||
+  if (prepare_kernel<SimtSmem<D>, tree_simt_kernel<D>>() != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, tree_simt_kernel<D>, kThreads,
                                                     sizeof(SimtSmem<D>)) != cudaSuccess ||
       n < 1)
