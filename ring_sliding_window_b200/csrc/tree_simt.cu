@@ -102,7 +102,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int kRows = Smem::kRows;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
-  constexpr int kRT = kRows / 16;       // rows of a thread
   constexpr int kCT = D / 64;           // groups of 4 output columns of a thread
   constexpr int kTPR = kThreads / kRows;  // threads of a row in the softmax
   constexpr int N = 4;  // elements of a 16-byte chunk
@@ -133,218 +132,231 @@ __global__ void __launch_bounds__(kThreads, 2)
       sm.limit[r] = v.W - 1 - tv.depth[i];
       sm.above[r] = tv.above[i];
     }
-    float m = -INFINITY, l = 0.f;  // of row tid / kTPR
-    uint64_t acc[kRT][kCT * 2];  // columns in pairs
+    // with rt rows a thread: no more than the sequence's drafts need
+    auto run = [&](auto rt) {
+      constexpr int kRT = decltype(rt)::value;
+      float m = -INFINITY, l = 0.f;  // of row tid / kTPR
+      uint64_t acc[kRT][kCT * 2];  // columns in pairs
 #pragma unroll
-    for (int i = 0; i < kRT; ++i)
+      for (int i = 0; i < kRT; ++i)
 #pragma unroll
-      for (int c = 0; c < kCT * 2; ++c) acc[i][c] = 0;
+        for (int c = 0; c < kCT * 2; ++c) acc[i][c] = 0;
 
-    for (int tl = pc.key_begin; tl < pc.key_end; ++tl) {
-      const bool drafts = tl < n_draft_tiles;
-      const int k0 = (drafts ? tl : tl - n_draft_tiles) * kKeys;  // first draft / slot
-      const int nk = drafts ? min(kKeys, n - k0) : min(kKeys, ring.held - k0);
-      if (nk <= 0 || (!drafts && k0 + kKeys <= ring.lo)) continue;  // nothing in it
-      __syncthreads();  // the previous tile's products are done
-      for (int e = tid; e < kKeys * (D / 2 / N); e += kThreads) {
-        const int r = e / (D / 2 / N), c = e % (D / 2 / N);
-        if (r >= nk) continue;  // masked below, its contents unused
-        if (drafts) {
-          const int64_t i = draft0 + k0 + r;
-          load_rotated<D>(a.kd + (i * v.H + pc.h) * D, sm.k[r], c,
-                          v.rope ? tv.cs + i * (D / 2) : nullptr);
-        } else {
-          load_rotated<D>(a.kc + (pc.row0 + k0 + r) * D, sm.k[r], c, nullptr);
-        }
-      }
-      // V: from memory to registers, and from there to shared memory (0 behind the
-      // last entry)
-      constexpr int kLoads = kKeys * (D / N) / kThreads;
-      float4 vreg[kLoads];
-      bool bad = false;  // a value that is not finite
-      auto fetch_v = [&]() {
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-          const int at = tid + e * kThreads, r = at / (D / N), c = at % (D / N) * N;
-          vreg[e] = r >= nk ? make_float4(0.f, 0.f, 0.f, 0.f)
-                            : *reinterpret_cast<const float4 *>(
-                                  drafts ? a.vd + ((draft0 + k0 + r) * v.H + pc.h) * D + c
-                                         : a.vc + (pc.row0 + k0 + r) * D + c);
-        }
-      };
-      auto store_v = [&]() {
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-          const int at = tid + e * kThreads, r = at / (D / N), c = at % (D / N) * N;
-          const float4 x = vreg[e];
-          bad |= !isfinite(x.x) || !isfinite(x.y) || !isfinite(x.z) || !isfinite(x.w);
-          *reinterpret_cast<float4 *>(&sm.v()[r][c]) = x;
-        }
-      };
-      if constexpr (!Smem::kShared) {
-        fetch_v();
-        store_v();
-      }
-      if (!drafts && tid < kKeys) sm.age[tid] = slot_age(ring, k0 + tid);
-      __syncthreads();
-      // scores of rows ty + 16 i against keys tx + 16 j
-      float s[kRT][4];
-#pragma unroll
-      for (int i = 0; i < kRT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-      auto scores = [&](auto count) {  // of the first 16 J keys
-        constexpr int J = decltype(count)::value;
-#pragma unroll 4
-        for (int c = 0; c < D; c += 4) {
-          float4 qv[kRT], kv[J];
-#pragma unroll
-          for (int i = 0; i < kRT; ++i)
-            qv[i] = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][c]);
-#pragma unroll
-          for (int j = 0; j < J; ++j)
-            kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][c]);
-#pragma unroll
-          for (int i = 0; i < kRT; ++i)
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-              s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-              s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-              s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-              s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
-            }
-        }
-      };
-      if (nk <= 16)
-        scores(Count<1>());
-      else if (nk <= 32)
-        scores(Count<2>());
-      else
-        scores(Count<4>());
-#pragma unroll
-      for (int i = 0; i < kRT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sm.p[ty + 16 * i][tx + 16 * j] = s[i][j] * qs;
-      __syncthreads();
-      if constexpr (Smem::kShared) fetch_v();  // behind the softmax
-      {
-        // softmax of row r by kTPR neighbouring threads
-        const int r = tid / kTPR, sub = tid % kTPR;
-        const int limit = sm.limit[r];
-        const uint4 ab = sm.above[r];
-        const uint32_t word[4] = {ab.x, ab.y, ab.z, ab.w};
-        bool see[kKeys / kTPR];
-        float x[kKeys / kTPR], mt = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < kKeys / kTPR; ++j) {
-          const int key = sub + kTPR * j;
-          x[j] = sm.p[r][key];
+      for (int tl = pc.key_begin; tl < pc.key_end; ++tl) {
+        const bool drafts = tl < n_draft_tiles;
+        const int k0 = (drafts ? tl : tl - n_draft_tiles) * kKeys;  // first draft / slot
+        const int nk = drafts ? min(kKeys, n - k0) : min(kKeys, ring.held - k0);
+        if (nk <= 0 || (!drafts && k0 + kKeys <= ring.lo)) continue;  // nothing in it
+        __syncthreads();  // the previous tile's products are done
+        for (int e = tid; e < kKeys * (D / 2 / N); e += kThreads) {
+          const int r = e / (D / 2 / N), c = e % (D / 2 / N);
+          if (r >= nk) continue;  // masked below, its contents unused
           if (drafts) {
-            const int node = k0 + key;
-            see[j] = key < nk && ((word[node >> 5 & 3] >> (node & 31)) & 1u);
+            const int64_t i = draft0 + k0 + r;
+            load_rotated<D>(a.kd + (i * v.H + pc.h) * D, sm.k[r], c,
+                            v.rope ? tv.cs + i * (D / 2) : nullptr);
           } else {
-            see[j] = key < nk && sm.age[key] <= limit;
+            load_rotated<D>(a.kc + (pc.row0 + k0 + r) * D, sm.k[r], c, nullptr);
           }
-          if (see[j]) mt = fmaxf(mt, x[j]);
         }
+        // V: from memory to registers, and from there to shared memory (0 behind the
+        // last entry)
+        constexpr int kLoads = kKeys * (D / N) / kThreads;
+        float4 vreg[kLoads];
+        bool bad = false;  // a value that is not finite
+        auto fetch_v = [&]() {
 #pragma unroll
-        for (int o = kTPR / 2; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-        const float m_new = fmaxf(m, mt);
-        // a row that has seen nothing yet keeps m = -inf, l = 0
-        const float sub_m = m_new == -INFINITY ? 0.f : m_new;
-        const float corr = exp2f(m - sub_m);
-        float lt = 0.f;
+          for (int e = 0; e < kLoads; ++e) {
+            const int at = tid + e * kThreads, r = at / (D / N), c = at % (D / N) * N;
+            vreg[e] = r >= nk ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : *reinterpret_cast<const float4 *>(
+                                    drafts ? a.vd + ((draft0 + k0 + r) * v.H + pc.h) * D + c
+                                           : a.vc + (pc.row0 + k0 + r) * D + c);
+          }
+        };
+        auto store_v = [&]() {
 #pragma unroll
-        for (int j = 0; j < kKeys / kTPR; ++j) {
-          const float w = see[j] ? exp2f(x[j] - sub_m) : 0.f;
-          lt += w;
-          sm.p[r][sub + kTPR * j] = w;
+          for (int e = 0; e < kLoads; ++e) {
+            const int at = tid + e * kThreads, r = at / (D / N), c = at % (D / N) * N;
+            const float4 x = vreg[e];
+            bad |= !isfinite(x.x) || !isfinite(x.y) || !isfinite(x.z) || !isfinite(x.w);
+            *reinterpret_cast<float4 *>(&sm.v()[r][c]) = x;
+          }
+        };
+        if constexpr (!Smem::kShared) {
+          fetch_v();
+          store_v();
         }
+        if (!drafts && tid < kKeys) sm.age[tid] = slot_age(ring, k0 + tid);
+        __syncthreads();
+        // scores of rows ty + 16 i against keys tx + 16 j
+        float s[kRT][4];
 #pragma unroll
-        for (int o = kTPR / 2; o > 0; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-        l = l * corr + lt;
-        m = m_new;
-        if (sub == 0) sm.alpha[r] = corr;
-      }
-      if constexpr (Smem::kShared) store_v();
-      bad = __syncthreads_or(bad) != 0;
+        for (int i = 0; i < kRT; ++i)
 #pragma unroll
-      for (int i = 0; i < kRT; ++i) {
-        const float corr = sm.alpha[ty + 16 * i];
+          for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+        auto scores = [&](auto count) {  // of the first 16 J keys
+          constexpr int J = decltype(count)::value;
+#pragma unroll 4
+          for (int c = 0; c < D; c += 4) {
+            float4 qv[kRT], kv[J];
 #pragma unroll
-        for (int c = 0; c < kCT * 2; ++c) acc[i][c] = tc::fmul2(acc[i][c], tc::f2_pack(corr, corr));
-      }
-      auto sees = [&](int row, int key) {
-        if (!drafts) return key < nk && sm.age[key] <= sm.limit[row];
-        const uint4 ab = sm.above[row];
-        const int node = k0 + key, w = node >> 5;
-        return key < nk &&
-               (((w == 0 ? ab.x : w == 1 ? ab.y : w == 2 ? ab.z : ab.w) >> (node & 31)) & 1u) != 0u;
-      };
-      auto products = [&](auto check) {
+            for (int i = 0; i < kRT; ++i)
+              qv[i] = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][c]);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+              kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][c]);
+#pragma unroll
+            for (int i = 0; i < kRT; ++i)
+#pragma unroll
+              for (int j = 0; j < J; ++j) {
+                s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+                s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+                s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+                s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+              }
+          }
+        };
+        if (nk <= 16)
+          scores(Count<1>());
+        else if (nk <= 32)
+          scores(Count<2>());
+        else
+          scores(Count<4>());
+#pragma unroll
+        for (int i = 0; i < kRT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sm.p[ty + 16 * i][tx + 16 * j] = s[i][j] * qs;
+        __syncthreads();
+        if constexpr (Smem::kShared) fetch_v();  // behind the softmax
+        {
+          // softmax of row r by kTPR neighbouring threads
+          const int r = tid / kTPR, sub = tid % kTPR;
+          const int limit = sm.limit[r];
+          const uint4 ab = sm.above[r];
+          const uint32_t word[4] = {ab.x, ab.y, ab.z, ab.w};
+          bool see[kKeys / kTPR];
+          float x[kKeys / kTPR], mt = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < kKeys / kTPR; ++j) {
+            const int key = sub + kTPR * j;
+            x[j] = sm.p[r][key];
+            if (drafts) {
+              const int node = k0 + key;
+              see[j] = key < nk && ((word[node >> 5 & 3] >> (node & 31)) & 1u);
+            } else {
+              see[j] = key < nk && sm.age[key] <= limit;
+            }
+            if (see[j]) mt = fmaxf(mt, x[j]);
+          }
+#pragma unroll
+          for (int o = kTPR / 2; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+          const float m_new = fmaxf(m, mt);
+          // a row that has seen nothing yet keeps m = -inf, l = 0
+          const float sub_m = m_new == -INFINITY ? 0.f : m_new;
+          const float corr = exp2f(m - sub_m);
+          float lt = 0.f;
+#pragma unroll
+          for (int j = 0; j < kKeys / kTPR; ++j) {
+            const float w = see[j] ? exp2f(x[j] - sub_m) : 0.f;
+            lt += w;
+            sm.p[r][sub + kTPR * j] = w;
+          }
+#pragma unroll
+          for (int o = kTPR / 2; o > 0; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+          l = l * corr + lt;
+          m = m_new;
+          if (sub == 0) sm.alpha[r] = corr;
+        }
+        if constexpr (Smem::kShared) store_v();
+        bad = __syncthreads_or(bad) != 0;
+#pragma unroll
+        for (int i = 0; i < kRT; ++i) {
+          const float corr = sm.alpha[ty + 16 * i];
+#pragma unroll
+          for (int c = 0; c < kCT * 2; ++c) acc[i][c] = tc::fmul2(acc[i][c], tc::f2_pack(corr, corr));
+        }
+        auto sees = [&](int row, int key) {
+          if (!drafts) return key < nk && sm.age[key] <= sm.limit[row];
+          const uint4 ab = sm.above[row];
+          const int node = k0 + key, w = node >> 5;
+          return key < nk &&
+                 (((w == 0 ? ab.x : w == 1 ? ab.y : w == 2 ? ab.z : ab.w) >> (node & 31)) & 1u) != 0u;
+        };
+        auto products = [&](auto check) {
 #pragma unroll 2
-        for (int j0 = 0; j0 < nk; j0 += 4) {
-          float4 w4[kRT];
+          for (int j0 = 0; j0 < nk; j0 += 4) {
+            float4 w4[kRT];
 #pragma unroll
-          for (int i = 0; i < kRT; ++i)
-            w4[i] = *reinterpret_cast<const float4 *>(&sm.p[ty + 16 * i][j0]);
+            for (int i = 0; i < kRT; ++i)
+              w4[i] = *reinterpret_cast<const float4 *>(&sm.p[ty + 16 * i][j0]);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            ulonglong2 vv[kCT];
+            for (int u = 0; u < 4; ++u) {
+              ulonglong2 vv[kCT];
 #pragma unroll
-            for (int c = 0; c < kCT; ++c)
-              vv[c] = *reinterpret_cast<const ulonglong2 *>(&sm.v()[j0 + u][tx * 4 + 64 * c]);
+              for (int c = 0; c < kCT; ++c)
+                vv[c] = *reinterpret_cast<const ulonglong2 *>(&sm.v()[j0 + u][tx * 4 + 64 * c]);
 #pragma unroll
-            for (int i = 0; i < kRT; ++i) {
-              const float w = u == 0 ? w4[i].x : u == 1 ? w4[i].y : u == 2 ? w4[i].z : w4[i].w;
-              if (!decltype(check)::value || sees(ty + 16 * i, j0 + u)) {
-                const uint64_t w2 = tc::f2_pack(w, w);
+              for (int i = 0; i < kRT; ++i) {
+                const float w = u == 0 ? w4[i].x : u == 1 ? w4[i].y : u == 2 ? w4[i].z : w4[i].w;
+                if (!decltype(check)::value || sees(ty + 16 * i, j0 + u)) {
+                  const uint64_t w2 = tc::f2_pack(w, w);
 #pragma unroll
-                for (int c = 0; c < kCT; ++c) {
-                  acc[i][2 * c] = tc::ffma2(w2, vv[c].x, acc[i][2 * c]);
-                  acc[i][2 * c + 1] = tc::ffma2(w2, vv[c].y, acc[i][2 * c + 1]);
+                  for (int c = 0; c < kCT; ++c) {
+                    acc[i][2 * c] = tc::ffma2(w2, vv[c].x, acc[i][2 * c]);
+                    acc[i][2 * c + 1] = tc::ffma2(w2, vv[c].y, acc[i][2 * c + 1]);
+                  }
                 }
               }
             }
           }
-        }
-      };
-      // an unseen entry's weight is 0; where its value would make 0 x inf of that it
-      // is left out one by one
-      if (!bad)
-        products(Count<0>());
-      else
-        products(Count<1>());
-    }
+        };
+        // an unseen entry's weight is 0; where its value would make 0 x inf of that it
+        // is left out one by one
+        if (!bad)
+          products(Count<0>());
+        else
+          products(Count<1>());
+      }
 
-    // the piece's result: final where it is the ring's only one, else a partial
-    __syncthreads();
-    if (tid % kTPR == 0) {
-      const int r = tid / kTPR;
-      if (pc.count == 1)
-        sm.alpha[r] = l;
-      else if (row0 + r < n)
-        tv.part_ml[(int64_t)p * tv.T + row0 + r] = make_float2(m, l);
-    }
-    __syncthreads();
+      // the piece's result: final where it is the ring's only one, else a partial
+      __syncthreads();
+      if (tid % kTPR == 0) {
+        const int r = tid / kTPR;
+        if (pc.count == 1)
+          sm.alpha[r] = l;
+        else if (row0 + r < n)
+          tv.part_ml[(int64_t)p * tv.T + row0 + r] = make_float2(m, l);
+      }
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kRT; ++i) {
-      const int r = row0 + ty + 16 * i;
-      if (r >= n) continue;
+      for (int i = 0; i < kRT; ++i) {
+        const int r = row0 + ty + 16 * i;
+        if (r >= n) continue;
 #pragma unroll
-      for (int c = 0; c < kCT; ++c) {
-        const int e = tx * 4 + 64 * c;
-        float4 x = make_float4(tc::f2_lo(acc[i][2 * c]), tc::f2_hi(acc[i][2 * c]),
-                               tc::f2_lo(acc[i][2 * c + 1]), tc::f2_hi(acc[i][2 * c + 1]));
-        if (pc.count == 1) {
-          const float sum = sm.alpha[ty + 16 * i];
-          x = make_float4(x.x / sum, x.y / sum, x.z / sum, x.w / sum);
-          *reinterpret_cast<float4 *>(a.out + ((draft0 + r) * v.H + pc.h) * D + e) = x;
-        } else {
-          *reinterpret_cast<float4 *>(tv.part_o + ((int64_t)p * tv.T + r) * D + e) = x;
+        for (int c = 0; c < kCT; ++c) {
+          const int e = tx * 4 + 64 * c;
+          float4 x = make_float4(tc::f2_lo(acc[i][2 * c]), tc::f2_hi(acc[i][2 * c]),
+                                 tc::f2_lo(acc[i][2 * c + 1]), tc::f2_hi(acc[i][2 * c + 1]));
+          if (pc.count == 1) {
+            const float sum = sm.alpha[ty + 16 * i];
+            x = make_float4(x.x / sum, x.y / sum, x.z / sum, x.w / sum);
+            *reinterpret_cast<float4 *>(a.out + ((draft0 + r) * v.H + pc.h) * D + e) = x;
+          } else {
+            *reinterpret_cast<float4 *>(tv.part_o + ((int64_t)p * tv.T + r) * D + e) = x;
+          }
         }
       }
-    }
+    };
+    const int rt = (min(kRows, n - row0) + 15) / 16;
+    if (rt == 1)
+      run(Count<1>());
+    else if (rt == 2)
+      run(Count<2>());
+    else if (rt == 3)
+      run(Count<3>());
+    else
+      run(Count<4>());
   }
 }
 
