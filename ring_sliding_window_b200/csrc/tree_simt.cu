@@ -20,7 +20,7 @@
 // More: tree_simt_kernel, row groups of 64.  A tile is 64 keys: 256 threads form
 // a 16 x 16 grid, each with 4 query rows x 4 keys of the scores, then the same
 // rows x D / 16 output columns.  Bound by FP32 FMA issue and the barriers between
-// its phases.  4 x 4,096 tokens: 184 us for 33 to 64 drafts, where the rows kernel
+// its phases.  4 x 4,096 tokens: 181 us for 33 to 64 drafts, where the rows kernel
 // takes 157 for 32 and twice that for 64.
 #include <cuda_runtime.h>
 #include <float.h>
@@ -71,7 +71,7 @@ struct Count {
 };
 
 // Elements 4 c .. 4 c + 3 of both halves of the row at `src` into dst, turned by
-// the (cos, sin) table cs if there is one (rotate-half RoPE).
+// the (cos, sin) table cs (rotate-half RoPE).
 template <int D>
 __device__ __forceinline__ void load_rotated(const float *src, float *dst, int c,
                                              const float2 *cs) {
@@ -81,12 +81,8 @@ __device__ __forceinline__ void load_rotated(const float *src, float *dst, int c
   Chunk<float>::widen(*reinterpret_cast<const uint4 *>(src + c * N + D / 2), b);
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    float x = a[e], y = b[e];
-    if (cs) {
-      const float2 r = cs[c * N + e];
-      x = a[e] * r.x - b[e] * r.y;
-      y = b[e] * r.x + a[e] * r.y;
-    }
+    const float2 r = cs[c * N + e];
+    const float x = a[e] * r.x - b[e] * r.y, y = b[e] * r.x + a[e] * r.y;
     a[e] = x;
     b[e] = y;
   }
@@ -121,11 +117,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     const RingView ring = ring_view(v, pc.b, pc.plen);
     const int64_t draft0 = (int64_t)pc.b * tv.T;  // first draft's row of [B][T]
     __syncthreads();  // the previous piece is done with shared memory
-    for (int e = tid; e < kRows * (D / 2 / N); e += kThreads) {
-      const int r = e / (D / 2 / N), c = e % (D / 2 / N);
-      const int64_t i = draft0 + min(row0 + r, n - 1);
-      load_rotated<D>(a.q + (i * v.H + pc.h) * D, sm.q[r], c,
-                         v.rope ? tv.cs + i * (D / 2) : nullptr);
+    if (v.rope) {
+      for (int e = tid; e < kRows * (D / 2 / N); e += kThreads) {
+        const int r = e / (D / 2 / N), c = e % (D / 2 / N);
+        const int64_t i = draft0 + min(row0 + r, n - 1);
+        load_rotated<D>(a.q + (i * v.H + pc.h) * D, sm.q[r], c, tv.cs + i * (D / 2));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kRows * (D / N) / kThreads; ++e) {
+        const int at = tid + e * kThreads, r = at / (D / N), c = at % (D / N) * N;
+        *reinterpret_cast<float4 *>(&sm.q[r][c]) = *reinterpret_cast<const float4 *>(
+            a.q + ((draft0 + min(row0 + r, n - 1)) * v.H + pc.h) * D + c);
+      }
     }
     for (int r = tid; r < kRows; r += kThreads) {
       const int64_t i = draft0 + min(row0 + r, n - 1);
@@ -148,32 +152,21 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int nk = drafts ? min(kKeys, n - k0) : min(kKeys, ring.held - k0);
         if (nk <= 0 || (!drafts && k0 + kKeys <= ring.lo)) continue;  // nothing in it
         __syncthreads();  // the previous tile's products are done
-        for (int e = tid; e < kKeys * (D / 2 / N); e += kThreads) {
-          const int r = e / (D / 2 / N), c = e % (D / 2 / N);
-          if (r >= nk) continue;  // masked below, its contents unused
-          if (drafts) {
-            const int64_t i = draft0 + k0 + r;
-            load_rotated<D>(a.kd + (i * v.H + pc.h) * D, sm.k[r], c,
-                            v.rope ? tv.cs + i * (D / 2) : nullptr);
-          } else {
-            load_rotated<D>(a.kc + (pc.row0 + k0 + r) * D, sm.k[r], c, nullptr);
-          }
-        }
-        // V: from memory to registers, and from there to shared memory (0 behind the
-        // last entry)
+        // K and V: from memory to registers, every load in flight, and from there to
+        // shared memory (0 behind the last entry)
         constexpr int kLoads = kKeys * (D / N) / kThreads;
-        float4 vreg[kLoads];
-        bool bad = false;  // a value that is not finite
-        auto fetch_v = [&]() {
+        auto fetch = [&](const float *drafted, const float *cached, float4 *x) {
 #pragma unroll
           for (int e = 0; e < kLoads; ++e) {
             const int at = tid + e * kThreads, r = at / (D / N), c = at % (D / N) * N;
-            vreg[e] = r >= nk ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : *reinterpret_cast<const float4 *>(
-                                    drafts ? a.vd + ((draft0 + k0 + r) * v.H + pc.h) * D + c
-                                           : a.vc + (pc.row0 + k0 + r) * D + c);
+            x[e] = r >= nk ? make_float4(0.f, 0.f, 0.f, 0.f)
+                           : *reinterpret_cast<const float4 *>(
+                                 drafts ? drafted + ((draft0 + k0 + r) * v.H + pc.h) * D + c
+                                        : cached + (pc.row0 + k0 + r) * D + c);
           }
         };
+        float4 vreg[kLoads];
+        bool bad = false;  // a value that is not finite
         auto store_v = [&]() {
 #pragma unroll
           for (int e = 0; e < kLoads; ++e) {
@@ -183,10 +176,23 @@ __global__ void __launch_bounds__(kThreads, 2)
             *reinterpret_cast<float4 *>(&sm.v()[r][c]) = x;
           }
         };
-        if constexpr (!Smem::kShared) {
-          fetch_v();
-          store_v();
+        if constexpr (!Smem::kShared) fetch(a.vd, a.vc, vreg);
+        if (drafts && v.rope) {
+          for (int e = tid; e < nk * (D / 2 / N); e += kThreads) {
+            const int r = e / (D / 2 / N), c = e % (D / 2 / N);
+            const int64_t i = draft0 + k0 + r;
+            load_rotated<D>(a.kd + (i * v.H + pc.h) * D, sm.k[r], c, tv.cs + i * (D / 2));
+          }
+        } else {
+          float4 kreg[kLoads];
+          fetch(a.kd, a.kc, kreg);
+#pragma unroll
+          for (int e = 0; e < kLoads; ++e) {
+            const int at = tid + e * kThreads;
+            *reinterpret_cast<float4 *>(&sm.k[at / (D / N)][at % (D / N) * N]) = kreg[e];
+          }
         }
+        if constexpr (!Smem::kShared) store_v();
         if (!drafts && tid < kKeys) sm.age[tid] = slot_age(ring, k0 + tid);
         __syncthreads();
         // scores of rows ty + 16 i against keys tx + 16 j
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int j = 0; j < 4; ++j) sm.p[ty + 16 * i][tx + 16 * j] = s[i][j] * qs;
         __syncthreads();
-        if constexpr (Smem::kShared) fetch_v();  // behind the softmax
+        if constexpr (Smem::kShared) fetch(a.vd, a.vc, vreg);  // behind the softmax
         {
           // softmax of row r by kTPR neighbouring threads
           const int r = tid / kTPR, sub = tid % kTPR;
