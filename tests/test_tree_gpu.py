@@ -202,11 +202,12 @@ def test_values_that_every_draft_sees_reach_it(dtype, d, bad):
     assert torch.equal(out[..., others], clean[..., others])
 
 
-@pytest.mark.parametrize("d,T", [(128, 4), (64, 20), (128, 40), (64, 100)])
-def test_dropped_copies_end_with_a_timeout_status(d, T):
+@pytest.mark.parametrize("dtype,d,T", [(BF, 128, 4), (BF, 64, 20), (BF, 128, 40), (BF, 64, 100),
+                                       (F32, 128, 4), (F32, 64, 20)])
+def test_dropped_copies_end_with_a_timeout_status(dtype, d, T):
     """With the kernel's cache copies dropped every wait runs out, and says so."""
     rswa = _rswa()
-    c = Case(BF, d, 1, 8, (200, 30), (3, 9), T)
+    c = Case(dtype, d, 1, 8, (200, 30), (3, 9), T)
     c.run()
     q, k, v = c.q.cuda(), c.k.cuda(), c.v.cuda()
     out = torch.empty_like(q)
