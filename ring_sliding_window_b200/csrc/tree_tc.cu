@@ -116,7 +116,10 @@ struct __align__(1024) TreeSmem {
   uint64_t pv_done;
   uint64_t o_done[2], o_free[2];  // a piece's last PV finished; its results taken
   uint64_t l_done[2];  // sums and m of a piece written
-  uint64_t turned;     // RoPE: a piece's queries and drafted keys turned
+  // RoPE: a piece's queries and drafted keys turned.  One for each Q buffer: the side
+  // warps may turn the next piece's before the MMA warp has looked at this one's, but
+  // come back to a buffer only after q_free, which follows that look.
+  uint64_t turned[S::kQBufs];
   uint64_t mma_done;
   uint32_t tmem_base;
   int dead;
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
     for (int s = 0; s < NQ; ++s) {
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_free[s], 1);
+      mbar_init(&sm.turned[s], 4);
     }
     for (int s = 0; s < NK; ++s) {
       mbar_init(&sm.k_full[s], 1);
@@ -311,7 +315,6 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
       mbar_init(&sm.l_done[s], S::kSoftWarps);
     }
     mbar_init(&sm.pv_done, 1);
-    mbar_init(&sm.turned, 4);
     mbar_init(&sm.mma_done, 1);
     sm.dead = 0;
     fence_mbar_init();
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
       if (pt.n == 0) continue;
       const int qs = active % NQ;
       if (!(ok = wait(&sm.q_full[qs], (active / NQ) & 1))) break;
-      if (v.rope && !(ok = wait(&sm.turned, active & 1))) break;
+      if (v.rope && !(ok = wait(&sm.turned[qs], (active / NQ) & 1))) break;
       const int o = active & 1;
       for (int j = 0; ok && j < pt.n; ++j, ++it) {
         const int s = it % NK;
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.turned);
+        if (lane == 0) mbar_arrive(&sm.turned[qs]);
       }
       bool mend = false;
       for (int j = 0; j < pt.n; ++j, ++it) {

@@ -381,6 +381,60 @@ def test_wide_trees_turn_with_rope(dtype, d, rope):
     assert c.st.check() == 0
 
 
+def _rotated(x, pos, theta):
+    """x [H, d] turned at position pos (rotate-half), in 64 bits."""
+    half = x.shape[-1] // 2
+    a = pos * theta ** (-2.0 * torch.arange(half, dtype=torch.float64) / x.shape[-1])
+    x0, x1 = x[..., :half].double(), x[..., half:].double()
+    return torch.cat([x0 * a.cos() - x1 * a.sin(), x1 * a.cos() + x0 * a.sin()], -1)
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("T", [5, 16, 20])
+@pytest.mark.parametrize("rope", [1, 2])
+def test_short_rings_turn_with_rope(dtype, d, T, rope):
+    """More rings than SMs, each of a few tiles at most, so a CTA turns one ring's queries
+    after another's while little else holds it up.  The queries and drafted keys that the
+    reference attends with are turned in 64 bits and rounded to the element type, as the
+    call documents.  The kernel turns them in fp32: sines and cosines to 2 steps, two products
+    and a sum, so 2^-21 of the vector's length at most, on q and on k.  In bf16 a component
+    within that of a rounding's border (1 in 2^14 of them; more than 4 along a path of 20 in
+    no case of 10^8) falls to the other side, one step (eps) away.  An error x of a score
+    changes the output by up to 2 x of the mass."""
+    rswa = _rswa()
+    B, H, W, theta = 100, 4, 16, 10000.0
+    rng = np.random.default_rng(T)
+    plens = [int(x) for x in rng.integers(0, 100, B)]
+    t = [int(x) for x in rng.integers(0, 40, B)]
+    n = [int(x) for x in rng.integers(0, T + 1, B)]
+    c = Case(dtype, d, H, W, plens, t, T, n=n)
+    c.st.set_rope(rope, theta)
+    out = c.run()
+    assert torch.equal(out, c.run())
+    m = c.model
+    for b in range(0, B, 3):
+        for i in {0, n[b] // 2, n[b] - 1}:
+            if not 0 <= i < n[b]:
+                continue
+            path = ref.path_of(c.parents[b], i)
+
+            def pos(e):
+                return plens[b] + ((t[b] + e) % W if rope == 2 else t[b] + e)
+
+            ks = [_rotated(c.k[b, x], pos(e), theta).to(dtype) for e, x in enumerate(path)]
+            qt = _rotated(c.q[b, i], pos(len(path) - 1), theta).to(dtype)
+            for h in range(H):
+                k, v = m.entries(b, h, ks, [c.v[b, x] for x in path])
+                o, mass = ref.attend(qt[h], k, v, c.scale)
+                qh = qt[h].double()
+                x = 2.0 ** -20 * float(qh.norm() * k.norm(dim=1).max()) * c.scale
+                if dtype == BF:
+                    x += 4 * torch.finfo(BF).eps * float(qh.abs().max() * k.abs().max()) * c.scale
+                lim = ref.tolerance(o, mass, dtype) + 2 * x * mass
+                err = (out[b, i, h].double() - o).abs()
+                assert bool((err <= lim).all()), (b, i, h, float((err / lim).max()))
+
+
 @pytest.mark.parametrize("dtype,d", KINDS)
 def test_commit_writes_the_path_and_nothing_else(dtype, d):
     L, H, W, plens, t, T = 3, 2, 6, (5, 9, 0, 4), (2, 11, 6, 30), 10
