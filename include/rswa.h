@@ -232,7 +232,9 @@ typedef enum rswa_attention_mode {
 
 /* Takes effect for the calls enqueued after it.  Switching mode re-uploads
  * the prefill work list with a synchronous copy (call it before enqueuing
- * work, not between calls in flight).  RSWA_EINVAL for an unknown mode. */
+ * work, not between calls in flight).  RSWA_EINVAL for an unknown mode, and
+ * for the standard mode if a layer holds what rswa_evict kept: the window goes
+ * by position, and the kept entries' slots are not their positions. */
 rswa_status rswa_state_set_attention(rswa_state *state, int32_t mode);
 
 /* ------------------------------------------------------------------------
@@ -499,7 +501,8 @@ rswa_status rswa_decode_step_scored(rswa_state *state, int32_t layer, const void
  * setting and the positions: generated token t keeps position P_b + t of the
  * uncut prompt, and under RSWA_ROPE_SLOT P_b + (t mod W).  Decode may start on
  * the layer at once.  Ring slots that src does not hold are not written.
- * RSWA_EINVAL also if either state is in the standard sliding-window mode;
+ * RSWA_EINVAL also if either state is in the standard sliding-window mode,
+ * which dst cannot be switched to afterwards either;
  * RSWA_ESTATE if src's layer was never filled. */
 rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, const float *score,
                        int32_t n_first, int32_t n_last, float *dst_score, int32_t *kept,

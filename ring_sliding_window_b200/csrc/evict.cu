@@ -477,7 +477,7 @@ rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, co
   dst->dv.rope_theta = src->dv.rope_theta;
   e = launch_rope_table(dst->dv, st);
   if (e != cudaSuccess) return from_cuda(e);
-  dst->layer_ready[l] = 1;
+  dst->layer_ready[l] = kLayerEvicted;
   return RSWA_OK;
 }
 

@@ -127,6 +127,11 @@ struct TreeView {
   float2 *cs;                // [B][T][D/2] (cos, sin) at every draft's position (RoPE)
 };
 
+// A layer's prompt entries: none yet; every one of the prompt (prefilled, or filled
+// by the caller of a resumed state); the entries that an eviction kept, whose slots
+// are not their positions.
+enum LayerFill : uint8_t { kLayerEmpty = 0, kLayerWhole = 1, kLayerEvicted = 2 };
+
 }  // namespace rswa
 
 struct rswa_state {
@@ -135,7 +140,7 @@ struct rswa_state {
   std::vector<int64_t> slot_base;  // first cache slot of each request
   int64_t pool_slots;              // slots the caches hold (per layer, K or V)
   std::vector<void *> k_cache, v_cache;
-  std::vector<uint8_t> layer_ready;  // prefilled or resumed
+  std::vector<uint8_t> layer_ready;  // what the layer's cache holds, a LayerFill
   void *workspace;
   size_t workspace_size;
   int device;

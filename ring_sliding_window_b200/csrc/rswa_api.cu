@@ -347,7 +347,7 @@ rswa_status rswa_state_create_pooled(const rswa_config *cfg, const int64_t *pref
   if (slot_base) s->pool_slots = pool_slots;
   s->k_cache.assign(k_cache, k_cache + cfg->num_layers);
   s->v_cache.assign(v_cache, v_cache + cfg->num_layers);
-  s->layer_ready.assign((size_t)cfg->num_layers, n_generated ? 1 : 0);
+  s->layer_ready.assign((size_t)cfg->num_layers, n_generated ? kLayerWhole : kLayerEmpty);
   s->workspace = workspace;
   s->workspace_size = workspace_size;
   s->device = dev;
@@ -487,7 +487,7 @@ rswa_status rswa_prefill(rswa_state *s, int32_t layer, const void *q, const void
       e = launch_prefill_simt(s->dv, qa, k, v, out, kca, st);
   }
   if (e != cudaSuccess) return from_cuda(e);
-  s->layer_ready[(size_t)layer] = 1;
+  s->layer_ready[(size_t)layer] = kLayerWhole;
   return RSWA_OK;
 }
 
@@ -616,6 +616,9 @@ rswa_status rswa_state_set_attention(rswa_state *s, int32_t mode) {
   if (!s) return RSWA_EINVAL;
   if (mode != RSWA_ATTN_RING && mode != RSWA_ATTN_STANDARD_SWA) return RSWA_EINVAL;
   const bool swa = mode == RSWA_ATTN_STANDARD_SWA;
+  // the window goes by position, and an eviction's slots are not positions
+  if (swa && std::count(s->layer_ready.begin(), s->layer_ready.end(), kLayerEvicted) > 0)
+    return RSWA_EINVAL;
   if (swa != (s->dv.swa != 0)) {
     // re-plan the prefill blocks: one query tile per block with the window
     if (current_device() != s->device) return RSWA_EINVAL;

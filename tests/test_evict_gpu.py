@@ -337,6 +337,36 @@ def test_evict_refusals():
             src.decode_step_scored(0, q, q, q, q.clone(), *bad)
 
 
+def test_standard_window_is_refused_after_an_eviction():
+    """The window goes by position and the kept entries' slots are not positions: the switch is
+    refused, changes nothing, and the ring mode may be set again."""
+    rswa = _rswa()
+    H, W, d, P, K, t = 2, 30, 128, 200, 50, 3
+    src = rswa.State(1, 1, H, d, W, (P,), dtype=BF, n_generated=(t,))
+    dst = rswa.State(1, 1, H, d, W, (K,), dtype=BF)
+    _fill_random(src, BF, 1, 9)
+    dst.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)  # nothing in it yet
+    dst.set_attention(rswa.RSWA_ATTN_RING)
+    src.evict_into(dst, 0, torch.rand(H * (P + W), device="cuda"))
+    q, kn, vn = (torch.randn(1, H, d, device="cuda").to(BF) for _ in range(3))
+    outs = [torch.empty_like(q) for _ in range(3)]
+    dst.decode_step(0, q, kn, vn, outs[0])
+    with pytest.raises(rswa.RswaError) as e:
+        dst.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)
+    assert e.value.status == rswa.RSWA_EINVAL
+    dst.decode_step(0, q, kn, vn, outs[1])
+    dst.set_attention(rswa.RSWA_ATTN_RING)
+    dst.decode_step(0, q, kn, vn, outs[2])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    for h in range(H):
+        held = K + t + 1
+        o, mass = ref.attend(q[0, h].cpu(), dst.cache_view(0, "k", 0, h)[:held].double().cpu(),
+                             dst.cache_view(0, "v", 0, h)[:held].double().cpu(), d ** -0.5)
+        assert bool(((outs[0][0, h].double().cpu() - o).abs() <= ref.tolerance(o, mass, BF)).all())
+    # the source keeps its whole prompt, and the choice
+    src.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)
+
+
 def test_scored_step_and_evict_in_a_graph():
     rswa = _rswa()
     H, W, d, P, K = 2, 5, 128, 300, 100
