@@ -287,7 +287,13 @@ int64_t rswa_cache_offset(const rswa_state *state, int32_t b, int32_t h, int64_t
  *            over tokens 0..i of its own sequence (no window).
  * Also stores k, v into cache slots [0, P_b) of this layer; the ring
  * counters are not touched.  All pointers 16-byte aligned.  Returns
- * RSWA_EINVAL for a bad layer or pointer. */
+ * RSWA_EINVAL for a bad layer or pointer.
+ * The first prefill of a state that rswa_evict filled ends what that left in
+ * it: positions count from P_b again, rswa_reset_ring goes back to the counters
+ * of rswa_state_create (call it before the new prompt's first step), and the
+ * other layers that hold kept entries have to be filled before they are used.
+ * (Whether it is the first is decided when the call is made: to be captured in a
+ * CUDA graph, it has to be called after the eviction was.) */
 rswa_status rswa_prefill(rswa_state *state, int32_t layer, const void *q, const void *k,
                          const void *v, void *out, void *stream);
 
@@ -318,8 +324,8 @@ rswa_status rswa_decode_step(rswa_state *state, int32_t layer, const void *q, co
  * the token's last layer.  Capturable in a CUDA graph. */
 rswa_status rswa_advance(rswa_state *state, void *stream);
 
-/* Restore every t_b to its value at rswa_state_create (0, or n_generated),
- * on the device; capturable.  Starts the batch's generation over without
+/* Restore every t_b to its value at rswa_state_create (0, or n_generated), or
+ * at the last rswa_evict into this state, on the device; capturable.  Starts the batch's generation over without
  * rebuilding the state (the caches are not touched). */
 rswa_status rswa_reset_ring(rswa_state *state, void *stream);
 
@@ -499,8 +505,8 @@ rswa_status rswa_decode_step_scored(rswa_state *state, int32_t layer, const void
  * 16-byte aligned pointers; nothing of dst may overlap src.  dst takes over the
  * ring counters (also as the value that rswa_reset_ring restores), the RoPE
  * setting and the positions: generated token t keeps position P_b + t of the
- * uncut prompt, and under RSWA_ROPE_SLOT P_b + (t mod W).  Decode may start on
- * the layer at once.  Ring slots that src does not hold are not written.
+ * uncut prompt, and under RSWA_ROPE_SLOT P_b + (t mod W).  Both stay so until
+ * dst is prefilled.  Decode may start on the layer at once.  Ring slots that src does not hold are not written.
  * RSWA_EINVAL also if either state is in the standard sliding-window mode,
  * which dst cannot be switched to afterwards either;
  * RSWA_ESTATE if src's layer was never filled. */

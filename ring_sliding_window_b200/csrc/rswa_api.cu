@@ -182,7 +182,7 @@ WsLayout layout_ws(const rswa_config *c, const int64_t *plen, const DecodePlan &
   WsLayout w;
   size_t off = 0;
   w.err = off;         off = align256(off + 2 * sizeof(int32_t));
-  w.t = off;           off = align256(off + 2 * B * sizeof(int64_t));  // t and its reset copy
+  w.t = off;           off = align256(off + 3 * B * sizeof(int64_t));  // t, its reset copy, as created
   w.plen = off;        off = align256(off + B * sizeof(int32_t));
   w.pos_base = off;    off = align256(off + B * sizeof(int32_t));
   w.slot_base = off;   off = align256(off + (B + 1) * sizeof(int64_t));
@@ -251,6 +251,29 @@ int choose_cluster_size(const rswa_config *c, const int64_t *plen, int num_sms) 
 }
 
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
+
+bool holds_eviction(const rswa_state *s) {
+  return std::count(s->layer_ready.begin(), s->layer_ready.end(), kLayerEvicted) > 0;
+}
+
+// Before a prompt is prefilled into a state that an eviction filled: positions
+// count from its own prompt lengths again, rswa_reset_ring goes back to the
+// counters it was created with, and the layers that still hold the old prompt's
+// entries wait for theirs.
+cudaError_t end_eviction(rswa_state *s, cudaStream_t st) {
+  if (!holds_eviction(s)) return cudaSuccess;
+  const size_t B = (size_t)s->cfg.batch;
+  cudaError_t e = cudaMemcpyAsync(s->dv.pos_base, s->dv.plen, B * sizeof(int32_t),
+                                  cudaMemcpyDeviceToDevice, st);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(s->dv.t + B, s->dv.t + 2 * B, B * sizeof(int64_t),
+                        cudaMemcpyDeviceToDevice, st);
+  if (e == cudaSuccess) e = launch_rope_table(s->dv, st);
+  if (e != cudaSuccess) return e;
+  std::replace(s->layer_ready.begin(), s->layer_ready.end(), (uint8_t)kLayerEvicted,
+               (uint8_t)kLayerEmpty);
+  return cudaSuccess;
+}
 
 }  // namespace
 
@@ -374,7 +397,7 @@ rswa_status rswa_state_create_pooled(const rswa_config *cfg, const int64_t *pref
   int max_plen = 0;
   for (int b = 0; b < B; ++b) {
     t[b] = n_generated ? n_generated[b] : 0;
-    t[B + b] = t[b];  // reset copy
+    t[B + b] = t[2 * B + b] = t[b];
     pl[b] = pb[b] = (int32_t)prefill_len[b];
     sb[b] = s->slot_base[(size_t)b];
     tb[b + 1] = tb[b] + prefill_len[b];
@@ -466,13 +489,15 @@ rswa_status rswa_prefill(rswa_state *s, int32_t layer, const void *q, const void
     return RSWA_EINVAL;
   if (current_device() != s->device) return RSWA_EINVAL;
   cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = end_eviction(s, st);
+  if (e != cudaSuccess) return from_cuda(e);
   void *kc = s->k_cache[(size_t)layer];
   void *vc = s->v_cache[(size_t)layer];
   const int64_t kc_rows = (int64_t)s->cfg.num_heads * s->pool_slots;
   // the tensor-core kernel stores the prompt K/V into the cache itself; the
   // CUDA-core kernel takes a separate cache-fill pass
   const bool fused_fill = s->cfg.dtype == RSWA_BF16 && s->cfg.head_dim == 128;
-  cudaError_t e = fused_fill ? cudaSuccess : launch_cache_fill(s->dv, k, v, kc, vc, st);
+  e = fused_fill ? cudaSuccess : launch_cache_fill(s->dv, k, v, kc, vc, st);
   // RoPE: rotated k overwrites the cache's prompt slots, rotated q goes to
   // `out`; attention then reads q from `out` and k from the cache
   const bool rope = s->dv.rope != RSWA_ROPE_NONE;
@@ -617,8 +642,7 @@ rswa_status rswa_state_set_attention(rswa_state *s, int32_t mode) {
   if (mode != RSWA_ATTN_RING && mode != RSWA_ATTN_STANDARD_SWA) return RSWA_EINVAL;
   const bool swa = mode == RSWA_ATTN_STANDARD_SWA;
   // the window goes by position, and an eviction's slots are not positions
-  if (swa && std::count(s->layer_ready.begin(), s->layer_ready.end(), kLayerEvicted) > 0)
-    return RSWA_EINVAL;
+  if (swa && holds_eviction(s)) return RSWA_EINVAL;
   if (swa != (s->dv.swa != 0)) {
     // re-plan the prefill blocks: one query tile per block with the window
     if (current_device() != s->device) return RSWA_EINVAL;

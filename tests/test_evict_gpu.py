@@ -337,6 +337,78 @@ def test_evict_refusals():
             src.decode_step_scored(0, q, q, q, q.clone(), *bad)
 
 
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("rope", [0, 1, 2])
+def test_a_state_that_took_an_eviction_serves_another_prompt(dtype, d, rope):
+    """Prefilled again, it gives bit for bit what a new state gives: positions and counters are
+    its own again.  A layer not prefilled yet is refused, and a later eviction counts from the
+    uncut prompt as the first one did."""
+    rswa = _rswa()
+    H, W, P, K, L, t = 2, 6, 70, 30, 2, 9
+    g = torch.Generator(device="cuda").manual_seed(rope)
+
+    def draw(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+    src = rswa.State(1, L, H, d, W, (P,), dtype=dtype, n_generated=(t,))
+    _fill_random(src, dtype, L, 10)
+    used, new = (rswa.State(1, L, H, d, W, (K,), dtype=dtype) for _ in range(2))
+    for st in (src, used, new):
+        if rope:
+            st.set_rope(rope)
+    score = torch.rand(H * (P + W), generator=g, device="cuda")
+
+    def evict_and_step():
+        out = []
+        for layer in range(L):
+            src.evict_into(used, layer, score)
+            o = torch.empty_like(first[layer][0])
+            used.decode_step(layer, *first[layer], o)
+            out.append(o)
+        return out
+
+    first = [[draw(1, H, d) for _ in range(3)] for _ in range(L)]
+    before = evict_and_step()
+    used.advance()
+    qkv = [[draw(K, H, d) for _ in range(3)] for _ in range(L)]
+    outs = [[torch.empty_like(qkv[0][0]) for _ in range(L)] for _ in range(2)]
+    used.prefill(0, *qkv[0], outs[0][0])
+    assert used.ring()[0] == [t + 1]  # a prefill leaves the counters alone
+    with pytest.raises(rswa.RswaError) as e:
+        used.decode_step(1, *first[1], torch.empty_like(first[1][0]))
+    assert e.value.status == rswa.RSWA_ESTATE
+    used.prefill(1, *qkv[1], outs[0][1])
+    used.reset_ring()
+    for layer in range(L):
+        new.prefill(layer, *qkv[layer], outs[1][layer])
+    assert used.ring()[0] == [0]
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    tree_ins = [draw(1, 4, H, d) for _ in range(3)]
+    for step in range(W + 2):
+        for layer in range(L):
+            x = [draw(1, H, d) for _ in range(3)]
+            o = [torch.empty_like(x[0]) for _ in range(2)]
+            for st, out in zip((used, new), o):
+                st.decode_step(layer, *x, out)
+            assert torch.equal(*o)
+        o = [torch.empty_like(tree_ins[0]) for _ in range(2)]
+        for st, out in zip((used, new), o):
+            tree = st.tree(4)
+            tree.set()
+            tree.attention(0, *tree_ins, out)
+            st.advance()
+        assert torch.equal(*o)
+    for x, y in zip(used.k_cache + used.v_cache, new.k_cache + new.v_cache):
+        assert torch.equal(_bits(x), _bits(y))
+    used.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)  # slots are positions again
+    used.set_attention(rswa.RSWA_ATTN_RING)
+    for a, b in zip(before, evict_and_step()):
+        assert torch.equal(a, b)
+    assert used.ring()[0] == [t]
+    assert used.check() == 0
+
+
 def test_standard_window_is_refused_after_an_eviction():
     """The window goes by position and the kept entries' slots are not positions: the switch is
     refused, changes nothing, and the ring mode may be set again."""
