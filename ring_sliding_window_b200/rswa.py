@@ -599,6 +599,12 @@ class Tree:
         self.workspace = torch.empty(wb, dtype=torch.uint8, device=state.workspace.device)
         self.handle = rswa_tree_create(state.handle, self.T, self.workspace, wb, stream)
 
+    def _open(self):
+        """The handle, which points into the state's: neither may be closed."""
+        if not self.handle or not self.state.handle:
+            raise RswaError(RSWA_EINVAL, "the tree or its state is closed")
+        return self.handle
+
     def _drafts(self, t, what):
         _require(t, what, self._shape, self.state.dtype, self.state._device)
 
@@ -608,14 +614,14 @@ class Tree:
             _require(parent, "parent", (st.B, self.T), torch.int32, st._device)
         if n_draft is not None:
             _require(n_draft, "n_draft", (st.B,), torch.int32, st._device)
-        rswa_tree_set(self.handle, parent, n_draft, stream)
+        rswa_tree_set(self._open(), parent, n_draft, stream)
 
     def attention(self, layer, q, k_draft, v_draft, out, stream=None):
         self._drafts(q, "q")
         self._drafts(k_draft, "k_draft")
         self._drafts(v_draft, "v_draft")
         self._drafts(out, "out")
-        rswa_tree_attention(self.handle, layer, q, k_draft, v_draft, out, stream)
+        rswa_tree_attention(self._open(), layer, q, k_draft, v_draft, out, stream)
 
     def commit(self, k_draft, v_draft, path, path_len, stream=None):
         st = self.state
@@ -626,10 +632,10 @@ class Tree:
             _require(t, "draft", shape, dtype, device)
         _require(path, "path", (st.B, self.T), torch.int32, st._device)
         _require(path_len, "path_len", (st.B,), torch.int32, st._device)
-        rswa_tree_commit(self.handle, k_draft, v_draft, path, path_len, stream)
+        rswa_tree_commit(self._open(), k_draft, v_draft, path, path_len, stream)
 
     def advance(self, stream=None):
-        rswa_tree_advance(self.handle, stream)
+        rswa_tree_advance(self._open(), stream)
 
     def close(self):
         h, self.handle = getattr(self, "handle", None), None

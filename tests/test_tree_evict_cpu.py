@@ -44,3 +44,46 @@ def test_reference_paths():
     import tree_reference as ref
     assert ref.path_of([-1, 0, 0, 2], 3) == [0, 2, 3]
     assert ref.path_of([-1, -1], 1) == [1]
+
+
+def test_a_tree_of_a_closed_state_is_refused(rswa, monkeypatch):
+    """The C tree points to the C state: once that is gone no call may reach the library.  The
+    library's calls are replaced here by ones that only note that they were made."""
+    import types
+
+    import torch
+
+    class StandIn(rswa.Tree):
+        def __del__(self):
+            pass
+
+    made = []
+    for name in ("set", "attention", "commit", "advance", "destroy"):
+        monkeypatch.setattr(rswa, f"rswa_tree_{name}", lambda *a, name=name: made.append(name))
+    B, T, H, d = 2, 3, 2, 64
+    st = types.SimpleNamespace(B=B, L=1, H=H, d=d, dtype=torch.float32, handle=1,
+                               _device=torch.device("cpu"))
+    tree = StandIn.__new__(StandIn)
+    tree.state, tree.T, tree._shape, tree.handle = st, T, (B, T, H, d), 2
+    x = [torch.zeros(B, T, H, d) for _ in range(4)]
+    path, n = torch.zeros(B, T, dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
+    calls = [lambda: tree.set(path, n), lambda: tree.attention(0, *x),
+             lambda: tree.commit(x[:1], x[1:2], path, n), lambda: tree.advance()]
+    for call in calls:
+        call()
+    assert made == ["set", "attention", "commit", "advance"]
+    made.clear()
+    st.handle = None  # as State.close() leaves it
+    for call in calls:
+        with pytest.raises(rswa.RswaError) as e:
+            call()
+        assert e.value.status == rswa.RSWA_EINVAL
+    assert made == []
+    tree.close()  # the tree's own memory is still there to be freed
+    assert made == ["destroy"]
+    st.handle = 1
+    for call in calls:  # a closed tree
+        with pytest.raises(rswa.RswaError) as e:
+            call()
+        assert e.value.status == rswa.RSWA_EINVAL
+    assert made == ["destroy"]
