@@ -501,7 +501,8 @@ rswa_status rswa_decode_step_scored(rswa_state *state, int32_t layer, const void
  *  dst_score : device float, rswa_score_bytes(dst), or NULL: the moved entries'
  *            scores.
  *  kept    : device int32 [H * sum_b P'_b]: the source slots of ring (b, h),
- *            ascending, at H sum_{b' < b} P'_b' + h P'_b.
+ *            ascending, at H sum_{b' < b} P'_b' + h P'_b; may be NULL if every
+ *            P'_b is 0.
  * 16-byte aligned pointers; nothing of dst may overlap src.  dst takes over the
  * ring counters (also as the value that rswa_reset_ring restores), the RoPE
  * setting and the positions: generated token t keeps position P_b + t of the

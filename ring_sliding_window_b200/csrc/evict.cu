@@ -405,9 +405,10 @@ rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, co
   if (a.batch != c.batch || a.num_layers != c.num_layers || a.num_heads != c.num_heads ||
       a.head_dim != c.head_dim || a.window != c.window || a.dtype != c.dtype)
     return RSWA_EINVAL;
-  if (!score || !kept || !aligned16(score) || !aligned16(kept) ||
-      (dst_score && !aligned16(dst_score)))
+  // (the list of a dst without prompt entries is empty: it may have no address)
+  if (!score || !aligned16(score) || !aligned16(kept) || (dst_score && !aligned16(dst_score)))
     return RSWA_EINVAL;
+  if (!kept && dst->dv.total_tokens > 0) return RSWA_EINVAL;
   if (n_first < 0 || n_last < 0) return RSWA_EINVAL;
   if (src->dv.swa || dst->dv.swa) return RSWA_EINVAL;
   for (int b = 0; b < a.batch; ++b) {

@@ -175,6 +175,30 @@ def test_evict_keeps_the_highest_scores(dtype, d, plens, keep, first, last, t, W
     assert dst.ring()[0] == list(t)
 
 
+@pytest.mark.parametrize("plens,t", [((40,), (5,)), ((0,), (9,)), ((0, 300, 1), (0, 2, 30))])
+def test_evict_that_keeps_no_prompt_entry(plens, t):
+    """The ring alone moves; the list of kept slots is empty and has no address."""
+    rswa = _rswa()
+    H, W, d, B = 2, 7, 64, len(plens)
+    src = rswa.State(B, 1, H, d, W, plens, dtype=F32, n_generated=t)
+    dst = rswa.State(B, 1, H, d, W, (0,) * B, dtype=F32)
+    _fill_random(src, F32, 1, 6)
+    for buf in dst.k_cache + dst.v_cache:
+        buf.fill_(5.0)
+    score = torch.rand(src.score_buffer().numel(), device="cuda")
+    out = torch.full((rswa.rswa_score_bytes(dst.handle) // 4,), 5.0, device="cuda")
+    kept = src.evict_into(dst, 0, score, 0, 0, out)
+    assert kept.numel() == 0
+    _check_evicted(src, dst, 0, score, out, kept, 0, 0, t, H)
+    assert dst.ring()[0] == list(t)
+    # a list that is not empty needs its address
+    one = rswa.State(B, 1, H, d, W, tuple(min(1, p) for p in plens), dtype=F32)
+    if sum(plens) > 0:
+        with pytest.raises(rswa.RswaError) as e:
+            rswa.rswa_evict(src.handle, one.handle, 0, score, 0, 0, None, None)
+        assert e.value.status == rswa.RSWA_EINVAL
+
+
 def test_evict_orders_every_float():
     """Signed zeros tie, infinities and denormals rank by value, NaN ranks last, and
     protected slots stay even at NaN."""
