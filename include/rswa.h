@@ -483,8 +483,10 @@ size_t rswa_score_bytes(const rswa_state *state);
  * that hold no entry are not touched.
  *  score_in, score_out : device, rswa_score_bytes() each, 16-byte aligned; may
  *            be the same buffer (they must not overlap otherwise).
- *  scratch : device, rswa_score_bytes(), 16-byte aligned; overwritten.  Calls
- *            that may run at the same time need one each.
+ *  scratch : device, rswa_score_bytes(), 16-byte aligned; overwritten.
+ * Decode steps of one state, scored or not, share its workspace: order them on
+ * one stream, whatever their scratch.  Steps of different states may run at the
+ * same time, with a scratch each.
  * Errors as rswa_decode_step. */
 rswa_status rswa_decode_step_scored(rswa_state *state, int32_t layer, const void *q,
                                     const void *k_new, const void *v_new, void *out,
