@@ -509,7 +509,10 @@ rswa_status rswa_decode_step_scored(rswa_state *state, int32_t layer, const void
  * ring counters (also as the value that rswa_reset_ring restores), the RoPE
  * setting and the positions: generated token t keeps position P_b + t of the
  * uncut prompt, and under RSWA_ROPE_SLOT P_b + (t mod W).  Both stay so until
- * dst is prefilled.  Decode may start on the layer at once.  Ring slots that src does not hold are not written.
+ * dst is prefilled.  A state built anew over dst's memory (rswa_state_create,
+ * rswa_state_create_pooled) counts positions from its own lengths: where the
+ * library applies RoPE, keep dst for as long as its requests run.  Decode may
+ * start on the layer at once.  Ring slots that src does not hold are not written.
  * RSWA_EINVAL also if either state is in the standard sliding-window mode,
  * which dst cannot be switched to afterwards either;
  * RSWA_ESTATE if src's layer was never filled. */
