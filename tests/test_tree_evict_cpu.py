@@ -46,6 +46,32 @@ def test_reference_paths():
     assert ref.path_of([-1, -1], 1) == [1]
 
 
+@pytest.mark.parametrize("n", [12, 300, 2000, 16000])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("positive", [False, True])
+def test_the_pair_bound_needs_the_second_half_of_a_weight(n, d, positive):
+    """Weights as bf16 pairs keep the bound of tree_reference.pair_tolerance; without the second
+    value, with it subtracted or doubled, some of the outputs break it."""
+    import torch
+
+    import tree_reference as ref
+    g = torch.Generator().manual_seed(n + d)
+    broken = {0.0: 0, -1.0: 0, 2.0: 0}
+    for _ in range(20 if n <= 2000 else 3):
+        q, k, v = (torch.randn(*s, generator=g).to(torch.bfloat16).double()
+                   for s in ((d,), (n, d), (n, d)))
+        if positive:
+            v = v.abs()
+        o, mass = ref.attend(q, k, v, d ** -0.5)
+        lim = ref.pair_tolerance(q, k, o, mass, d ** -0.5)
+        assert bool(((ref.pair_attend(q, k, v, d ** -0.5) - o).abs() <= lim).all())
+        for lo in broken:
+            err = (ref.pair_attend(q, k, v, d ** -0.5, lo) - o).abs()
+            broken[lo] += int((err > lim).sum())
+    if positive or n <= 300:  # (sums that cancel hide it among many entries)
+        assert all(x > 0 for x in broken.values()), broken
+
+
 def test_a_tree_of_a_closed_state_is_refused(rswa, monkeypatch):
     """The C tree points to the C state: once that is gone no call may reach the library.  The
     library's calls are replaced here by ones that only note that they were made."""

@@ -229,6 +229,39 @@ def test_large_scores(dtype, d):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("T,plens,t", [(3, (40, 300), (2, 50)), (16, (2000,), (9,)),
+                                       (20, (500, 129), (0, 70)), (64, (700, 30), (20, 33)),
+                                       (100, (900,), (64,)), (7, (9000,), (100,))])
+@pytest.mark.parametrize("growing", [False, True])
+def test_both_halves_of_a_weight_count(d, T, plens, t, growing):
+    """bf16 against the bound that weights as pairs keep and single bf16 weights do not
+    (test_tree_evict_cpu.py): values of one sign, so nothing cancels, rings in one piece and in
+    several, and scores that grow along the keys, where the subtracted maximum moves and both
+    halves of the sums so far are scaled."""
+    c = Case(BF, d, 2, 64, plens, t, T, seed=40 + T)
+    m = c.model
+    for b, P in enumerate(plens):
+        m.pv[b] = m.pv[b].abs()
+        m.gv[b] = [x.abs() for x in m.gv[b]]
+        if growing:
+            ramp = torch.linspace(0, 60, P)[:, None, None]
+            m.pk[b] = (m.pk[b].float() * 0.05 +
+                       ramp * torch.sign(c.q[b, 0].float()) / d ** 0.5).to(BF)
+    c.v = c.v.abs()
+    m.fill(c.st)
+    out = c.run()
+    for b in range(len(plens)):
+        for i in sorted({0, 1, T // 2, T - 1}):
+            path = ref.path_of(c.parents[b], i)
+            for h in range(2):
+                k, v = m.entries(b, h, [c.k[b, x] for x in path], [c.v[b, x] for x in path])
+                o, mass = ref.attend(c.q[b, i, h], k, v, c.scale)
+                err = (out[b, i, h].double() - o).abs()
+                lim = ref.pair_tolerance(c.q[b, i, h], k, o, mass, c.scale)
+                assert bool((err <= lim).all()), (b, i, h, float((err / lim).max()))
+
+
 @pytest.mark.parametrize("dtype,d", KINDS)
 @pytest.mark.parametrize("rope", [0, 1, 2])
 @pytest.mark.parametrize("swa", [False, True])

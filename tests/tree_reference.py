@@ -79,6 +79,37 @@ def tolerance(ref, mass, dtype):
     return 2.0 ** -8 * (mass + ref.abs()) * 1.01 + 1e-5 * (1 + mass)
 
 
+def bf16_half_step(x):
+    """Half the distance between the bf16 values around |x|."""
+    return torch.exp2(torch.floor(torch.log2(x.abs().clamp_min(2.0 ** -126))) - 8)
+
+
+def pair_tolerance(q, k, ref, mass, scale):
+    """bf16 with every weight as a sum hi + lo of two bf16 values, both cut off: lo misses less
+    than 2^-7 of a rest that is less than 2^-7 of the weight, so 2^-14 of the mass.  The sums,
+    counted as one fp32 cut-off (2^-23) for every 16 products and a few more within those: a
+    score's d / 16 + 8 <= 16 of its products' absolute sum S, which change weights and their
+    sum alike, and the output's n / 16 + 8 of the mass.  Then one rounding of the output."""
+    s_abs = float((k.abs() @ q.double().abs()).max()) * scale
+    part = 1.01 * 2.0 ** -14 + 2.0 ** -23 * (2 * 16 * s_abs + k.shape[0] / 16 + 8)
+    err = part * mass
+    return bf16_half_step(ref.abs() + err) + err
+
+
+def cut_bf16(w):
+    """fp32 values with the lower half of their bits 0."""
+    return (w.float().view(torch.int32) & -65536).view(torch.float32)
+
+
+def pair_attend(q, k, v, scale, lo=1.0):
+    """The output in bf16 with weights hi + lo as in pair_tolerance, `lo` times the second."""
+    s = (k @ q.double()) * scale
+    w = torch.exp(s - s.max()).float()
+    hi = cut_bf16(w)
+    pair = hi.double() + lo * cut_bf16(w - hi).double()
+    return ((pair @ v) / w.double().sum()).to(torch.bfloat16).double()
+
+
 def random_parents(rng, T, reach=6):
     return [int(rng.integers(max(-1, i - reach), i)) if i else -1 for i in range(T)]
 
