@@ -118,6 +118,74 @@ def test_scored_steps_in_the_standard_window(dtype, d):
             assert np.all(np.isnan(f64(st.score_view(after, b, h))[held:]))
 
 
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("split", ["streamk", "cluster"])
+@pytest.mark.parametrize("rope", [0, 1, 2])
+def test_scored_steps_with_rope_over_a_pool(dtype, d, split, rope, monkeypatch):
+    """Requests placed out of order in a pool whose other slots, and their scores, hold NaN.  The
+    weights are those of the keys that the step left in the cache, turned there, and of the
+    query turned in 64 bits; the kernel turns it in fp32, 2^-21 of its length off at most, which
+    moves a score by that times the longest key, and a weight (at most 1) by twice as much."""
+    rswa = _rswa()
+    monkeypatch.setenv("RSWA_DECODE_SPLIT", split)
+    H, W, plens, t, steps, theta = 2, 6, (130, 7, 1500), (0, 11, 4), 15, 10000.0
+    B = len(plens)
+    pool = rswa.TokenPool(2400, 1, H, d, W, dtype=dtype)
+    for x in pool.k_cache + pool.v_cache:
+        x.fill_(float("nan"))
+    pool.alloc(20)
+    bases = {p: pool.alloc(p) for p in (7, 1500, 130)}
+    st = pool.state(plens, [bases[p] for p in plens], n_generated=t)
+    twin_pool = rswa.TokenPool(2400, 1, H, d, W, dtype=dtype)
+    m = ref.Model(plens, W, H, d, dtype, seed=12).generate(t)
+    m.fill(st)
+    for x, y in zip(twin_pool.k_cache + twin_pool.v_cache, pool.k_cache + pool.v_cache):
+        x.copy_(y)
+    twin = twin_pool.state(plens, [bases[p] for p in plens], n_generated=t)
+    for x in (st, twin):
+        x.set_rope(rope, theta)
+    score, scratch = st.score_buffer().fill_(float("nan")), st.score_buffer()
+    want, mine = {}, torch.zeros(score.numel(), dtype=torch.bool, device="cuda")
+    for b, P in enumerate(plens):
+        for h in range(H):
+            held = P + min(t[b], W)
+            st.score_view(score, b, h)[:held] = 0.5
+            st.score_view(mine, b, h)[:] = True
+            want[b, h] = np.full(P + W, 0.5)
+    slack = 0.0
+    for step in range(steps):
+        q, kn, vn = (m.draw(B, H, d).cuda() for _ in range(3))
+        out, out2 = torch.empty_like(q), torch.empty_like(q)
+        st.decode_step_scored(0, q, kn, vn, out, score, score, scratch)
+        twin.decode_step(0, q, kn, vn, out2)
+        assert torch.equal(out, out2)
+        for b, P in enumerate(plens):
+            now = t[b] + step
+            held, fresh = P + min(now + 1, W), P + now % W
+            pos = P + (now % W if rope == 2 else now)
+            for h in range(H):
+                k = st.cache_view(0, "k", b, h)[:held].double().cpu()
+                x = q[b, h].double().cpu()
+                if rope:
+                    half = d // 2
+                    angle = pos * theta ** (-2.0 * torch.arange(half, dtype=torch.float64) / d)
+                    x = torch.cat([x[:half] * angle.cos() - x[half:] * angle.sin(),
+                                   x[half:] * angle.cos() + x[:half] * angle.sin()])
+                    slack = max(slack, 2.0 ** -20 * float(x.norm() * k.norm(dim=1).max()) * d ** -0.5)
+                want[b, h][fresh] = 0.0
+                want[b, h][:held] += torch.softmax(k @ x * d ** -0.5, 0).numpy()
+                got = f64(st.score_view(score, b, h))
+                lim = (step + 1) * (2e-6 + (step + 2) * 2.0 ** -24 + slack)
+                assert np.max(np.abs(got[:held] - want[b, h][:held])) <= lim
+                assert np.all(np.isnan(got[held:]))
+        assert bool(score[~mine].isnan().all())
+        st.advance()
+        twin.advance()
+    for x, y in zip(pool.k_cache + pool.v_cache, twin_pool.k_cache + twin_pool.v_cache):
+        assert torch.equal(_bits(x), _bits(y))
+    assert st.check() == 0
+
+
 def _fill_random(st, dtype, layers, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
     for layer in range(layers):
