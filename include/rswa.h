@@ -396,7 +396,8 @@ rswa_status rswa_ngram_topk(float *logits, int64_t ld, const int32_t *history, i
  * that the caller's model confirmed into the rings of all layers, and
  * rswa_tree_advance adds its length to the ring counters.  With RoPE on, q and
  * k_draft are turned at their nodes' positions, and the cache receives turned
- * keys; a turned q or key counts as rounded to the element type.
+ * keys; a turned q or key counts as rounded to the element type (a decode step
+ * keeps its turned q in fp32).
  *
  * One step:  rswa_tree_set, rswa_tree_attention once a layer, rswa_tree_commit,
  * rswa_tree_advance.  All four may be captured in a CUDA graph.  Calls on one

@@ -68,9 +68,11 @@ __global__ void __launch_bounds__(kFinishThreads)
 // memory (beyond kSelCache entries they are read again, from L2), and every loop
 // after the first takes four a thread.
 //
-// Bound by instruction issue (about 100 an entry and lane over five loops) and,
-// for short rings, by the latency of seven short phases: 19 us for 40 rings of
-// 32,640 entries, 9 us for 80 of 8,256.  Clusters of 2 and 4 CTAs a ring, adding
+// Takes 19 us for 40 rings of 32,640 entries, on 40 SMs (8.0 until the first
+// counts, 9.5 in the four loops after that), and 9 us for 80 of 8,256; short
+// rings pay the latency of seven short phases.  The launch bound holds the kernel
+// to 32 registers, with spills of 12 bytes stored and 24 loaded; whether more
+// registers would help has not been measured.  Clusters of 2 and 4 CTAs a ring, adding
 // their counts through distributed shared memory, cost 10 us more: their barriers
 // and remote loads take longer than the loops that they share.
 constexpr int kSelMaxThreads = 1024;

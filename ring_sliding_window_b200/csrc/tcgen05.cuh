@@ -54,9 +54,9 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_
       : "memory");
 }
 
-// One lane of a converged warp.  A branch that only one thread takes makes the
-// issue of an MMA cost 62 cycles (operands cross to the uniform registers one by
-// one); a converged warp with this predicate issues one in 27.
+// One lane of a converged warp.  In a branch that only one thread takes the issue
+// of an MMA costs 62 cycles; a converged warp with this predicate issues one in 27
+// (128 MMAs with M = 128 and K = 16 in a row).
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t x;
   asm volatile(

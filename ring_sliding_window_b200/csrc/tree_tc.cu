@@ -6,8 +6,9 @@
 //   o_i = sum_j 2^(x_ij) v_j / sum_j 2^(x_ij),   x_ij = scale log2(e) q_i.k_j - m_i,
 // in one pass over K and V.  T drafts do 4 T d operations on the 4 d bytes of
 // an entry, so up to T = 128 the tensor cores (about 250 operations a byte)
-// wait for HBM: the kernel's job is to keep the copies coming and everything
-// else behind them.
+// could wait for HBM: the kernel's job is to keep the copies coming and
+// everything else behind them.  Up to 64 drafts it does on long prompts (1.2 to
+// 1.35 times the time of the bytes at 8 x 8,256 and 4 x 16,384 or 32,640 tokens).
 //
 // The 128-key tiles of all rings (a ring's drafts first, then its cache) are
 // cut into one range of about equal cost per CTA, one CTA an SM; a ring in several
@@ -30,11 +31,16 @@
 // More than 64 drafts are two columns of the grid with N = 64: half the SMs
 // each, over the same tiles at the same time, so HBM is read about once.  (One
 // CTA with N = 128 has no registers and shared memory left to keep the tensor
-// cores busy: 140 us against 111 for 128 drafts over 4 x 16,384 tokens.)
+// cores busy: 140 us against 111 for 128 drafts over 4 x 16,384 tokens.)  What
+// bounds them is the work on a tile: 70 tiles an SM, about 1.4 us each, and both
+// columns take every tile, which an SM's share of HBM brings in 1.5 us (the bytes
+// alone: 52 us).
 //
 // P goes to the MMA as a bf16 pair hi + lo, next to one another along N, so one
 // product gives O_hi | O_lo (relative error of a weight 2^-14 at most; bf16 alone
-// would add its 2^-9 to an output that is rounded to bf16 once).  O_hi is finite
+// would add its 2^-9 to an output that is rounded to bf16 once).  Both are cut off,
+// never rounded up, and the sum takes the uncut weights, so outputs lie about
+// 1e-5 of themselves too close to 0: less than a hundredth of their rounding.  O_hi is finite
 // wherever the exact sum is, and alone decides what is not: O_lo of an infinite
 // value is 0 x inf = NaN.
 //
