@@ -233,8 +233,9 @@ typedef enum rswa_attention_mode {
 /* Takes effect for the calls enqueued after it.  Switching mode re-uploads
  * the prefill work list with a synchronous copy (call it before enqueuing
  * work, not between calls in flight).  RSWA_EINVAL for an unknown mode, and
- * for the standard mode if a layer holds what rswa_evict kept: the window goes
- * by position, and the kept entries' slots are not their positions. */
+ * for the standard mode if a layer holds what rswa_evict kept, or a captured
+ * eviction may put it there: the window goes by position, and the kept entries'
+ * slots are not their positions. */
 rswa_status rswa_state_set_attention(rswa_state *state, int32_t mode);
 
 /* ------------------------------------------------------------------------
@@ -292,8 +293,10 @@ int64_t rswa_cache_offset(const rswa_state *state, int32_t b, int32_t h, int64_t
  * it: positions count from P_b again, rswa_reset_ring goes back to the counters
  * of rswa_state_create (call it before the new prompt's first step), and the
  * other layers that hold kept entries have to be filled before they are used.
- * (Whether it is the first is decided when the call is made: to be captured in a
- * CUDA graph, it has to be called after the eviction was.) */
+ * (This is decided when the call is made.  Once an eviction into the state has
+ * been captured in a CUDA graph, every later prefill does it, since a replay may
+ * have come before; a prefill that is itself captured before the first call of
+ * rswa_evict never does.) */
 rswa_status rswa_prefill(rswa_state *state, int32_t layer, const void *q, const void *k,
                          const void *v, void *out, void *stream);
 

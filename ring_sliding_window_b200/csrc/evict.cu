@@ -440,6 +440,9 @@ rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, co
     return RSWA_ENOMEM;
   }
   const cudaStream_t st = (cudaStream_t)stream;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(st, &capture);
+  if (e != cudaSuccess) return from_cuda(e);
   const unsigned rings = (unsigned)(a.batch * a.num_heads);
   const int max_p = src->dv.max_plen;
   const SelectArgs sel{src->dv, dst->dv, score, n_first, n_last, kept,
@@ -455,7 +458,7 @@ rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, co
   // about four entries a thread, in the longest ring, until a CTA is full
   int threads = 128;
   while (threads < kSelMaxThreads && threads * 4 < max_p) threads *= 2;
-  cudaError_t e = launch_overlapped(evict_select_kernel, dim3(rings), dim3((unsigned)threads),
+  e = launch_overlapped(evict_select_kernel, dim3(rings), dim3((unsigned)threads),
                                     (size_t)(kSelBins + sel.cache) * sizeof(uint32_t), st, sel);
   if (e != cudaSuccess) return from_cuda(e);
   MoveArgs mv;
@@ -481,6 +484,7 @@ rswa_status rswa_evict(const rswa_state *src, rswa_state *dst, int32_t layer, co
   e = launch_rope_table(dst->dv, st);
   if (e != cudaSuccess) return from_cuda(e);
   dst->layer_ready[l] = kLayerEvicted;
+  if (capture != cudaStreamCaptureStatusNone) dst->evict_captured = true;
   return RSWA_OK;
 }
 

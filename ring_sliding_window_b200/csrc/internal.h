@@ -141,6 +141,7 @@ struct rswa_state {
   int64_t pool_slots;              // slots the caches hold (per layer, K or V)
   std::vector<void *> k_cache, v_cache;
   std::vector<uint8_t> layer_ready;  // what the layer's cache holds, a LayerFill
+  bool evict_captured = false;       // a graph holds an eviction into it: any replay may fill it
   void *workspace;
   size_t workspace_size;
   int device;

@@ -253,10 +253,11 @@ int choose_cluster_size(const rswa_config *c, const int64_t *plen, int num_sms) 
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 
 bool holds_eviction(const rswa_state *s) {
-  return std::count(s->layer_ready.begin(), s->layer_ready.end(), kLayerEvicted) > 0;
+  return s->evict_captured ||
+         std::count(s->layer_ready.begin(), s->layer_ready.end(), kLayerEvicted) > 0;
 }
 
-// Before a prompt is prefilled into a state that an eviction filled: positions
+// Before a prompt is prefilled into a state that an eviction (may have) filled: positions
 // count from its own prompt lengths again, rswa_reset_ring goes back to the
 // counters it was created with, and the layers that still hold the old prompt's
 // entries wait for theirs.

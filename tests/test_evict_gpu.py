@@ -501,6 +501,56 @@ def test_a_state_that_took_an_eviction_serves_another_prompt(dtype, d, rope):
     assert used.check() == 0
 
 
+def test_captured_evictions_and_prefills_in_turn():
+    """A replay fills the state without a call that the host could note: every prefill after it
+    still starts over, called eagerly or replayed itself, and the standard window stays refused."""
+    rswa = _rswa()
+    H, W, d, P, K, t = 2, 5, 128, 90, 30, 11
+    src = rswa.State(1, 1, H, d, W, (P,), dtype=BF, n_generated=(t,))
+    src.set_rope(rswa.RSWA_ROPE_ABSOLUTE)
+    _fill_random(src, BF, 1, 13)
+    dst, new = (rswa.State(1, 1, H, d, W, (K,), dtype=BF) for _ in range(2))
+    new.set_rope(rswa.RSWA_ROPE_ABSOLUTE)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    score = torch.rand(H * (P + W), generator=g, device="cuda")
+    kept = torch.empty(H * K, dtype=torch.int32, device="cuda")
+    qkv = [torch.randn(K, H, d, generator=g, device="cuda").to(BF) for _ in range(3)]
+    x = [torch.randn(1, H, d, generator=g, device="cuda").to(BF) for _ in range(3)]
+    out, pre = torch.empty_like(x[0]), torch.empty_like(qkv[0])
+    new.prefill(0, *qkv, torch.empty_like(pre))
+    want = torch.empty_like(out)
+    new.decode_step(0, *x, want)
+    src.evict_into(dst, 0, score, kept=kept)  # warm-up
+    dst.prefill(0, *qkv, pre)
+    torch.cuda.synchronize()
+    evict, fill = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(evict):
+        src.evict_into(dst, 0, score, kept=kept)
+    with torch.cuda.graph(fill):
+        dst.prefill(0, *qkv, pre)
+
+    def fresh():
+        dst.reset_ring()
+        assert dst.ring()[0] == [0]
+        out.fill_(7.0)
+        dst.decode_step(0, *x, out)
+        assert torch.equal(out, want)
+
+    for again in range(3):
+        evict.replay()
+        assert dst.ring()[0] == [t]
+        dst.prefill(0, *qkv, pre)
+        fresh()
+        evict.replay()
+        assert dst.ring()[0] == [t]
+        fill.replay()
+        fresh()
+        with pytest.raises(rswa.RswaError) as e:
+            dst.set_attention(rswa.RSWA_ATTN_STANDARD_SWA)
+        assert e.value.status == rswa.RSWA_EINVAL
+    assert dst.check() == 0
+
+
 def test_standard_window_is_refused_after_an_eviction():
     """The window goes by position and the kept entries' slots are not positions: the switch is
     refused, changes nothing, and the ring mode may be set again."""
