@@ -328,8 +328,9 @@ rswa_status rswa_decode_step(rswa_state *state, int32_t layer, const void *q, co
 rswa_status rswa_advance(rswa_state *state, void *stream);
 
 /* Restore every t_b to its value at rswa_state_create (0, or n_generated), or
- * at the last rswa_evict into this state, on the device; capturable.  Starts the batch's generation over without
- * rebuilding the state (the caches are not touched). */
+ * at the last rswa_evict into this state, on the device; capturable.  Starts the
+ * batch's generation over without rebuilding the state (the caches are not
+ * touched). */
 rswa_status rswa_reset_ring(rswa_state *state, void *stream);
 
 /* Windowed no-repeat n-gram ban [§2.3].

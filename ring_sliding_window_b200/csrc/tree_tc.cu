@@ -40,7 +40,7 @@
 // product gives O_hi | O_lo (relative error of a weight 2^-14 at most; bf16 alone
 // would add its 2^-9 to an output that is rounded to bf16 once).  Both are cut off,
 // never rounded up, and the sum takes the uncut weights, so outputs lie about
-// 1e-5 of themselves too close to 0: less than a hundredth of their rounding.  O_hi is finite
+// 1e-5 of themselves too close to 0, a hundredth of their rounding.  O_hi is finite
 // wherever the exact sum is, and alone decides what is not: O_lo of an infinite
 // value is 0 x inf = NaN.
 //
